@@ -1,0 +1,138 @@
+/*
+ * xlstm_layer.h -- C ABI of the operators around the mLSTM cell (sm_100a): linear
+ * attention with a fixed decay per head, and the per-head group norm with an
+ * activation that brings a cell's output into channels-last order.
+ *
+ * Status codes, dtypes and conventions are those of xlstm_mlstm.h: every pointer is
+ * caller-owned device memory of the current device, the library allocates nothing,
+ * calls enqueue on `stream` and return without synchronising, argument problems are
+ * reported before anything is enqueued, and the first 16 bytes of a workspace are the
+ * device status block that xlstm_mlstm_workspace_status() reads.  All calls can be
+ * captured in a CUDA graph.  A workspace belongs to one call at a time: calls (or
+ * replays of graphs) that may overlap on the device need one each.
+ *
+ * ---- linear attention with a decay per head -----------------------------------
+ *
+ *   C_t = l_h C_{t-1} + v_t k_t^T,      o_t = scale C_t q_t,      l_h = exp(log_decay[h])
+ *
+ * i.e. the matrix memory of the mLSTM with a constant forget factor per head, no input
+ * gate and no normaliser.  The decay is a constant of the head and has no gradient.
+ *
+ * Layouts (row-major, contiguous):
+ *   q, k       [B][H][T][d_qk]   qkv_dtype (bf16 or fp32)
+ *   v, o       [B][H][T][d_v]    qkv_dtype
+ *   log_decay  [H]               fp32; 0 is no decay, -inf a head without memory; values
+ *                                above 0 are read as 0
+ *   lens       [B]               int32, or NULL: sequence b has lens[b] tokens (read as 0
+ *                                where negative and as T above T)
+ *   C          [B][H][d_v][d_qk] fp32, row = value index
+ * With lens, tokens at or past lens[b] take no part, whatever q, k, v hold there (NaN
+ * included); their rows of o, dq, dk and dv are written as zeros, and the final state is
+ * the one after token lens[b] - 1.
+ *
+ * log_decay and lens need 4-byte alignment, every other pointer 16-byte alignment.
+ */
+#ifndef XLSTM_LAYER_H
+#define XLSTM_LAYER_H
+
+#include "xlstm_mlstm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int32_t B, H;        /* batch, heads: >= 1; B * H * ceil(T / 64) at most 2^25        */
+    int32_t T;           /* padded sequence length: 0 to 2^30 (ignored by the step call) */
+    int32_t d_qk, d_v;   /* head dims: multiples of 16 in [16, 512]                      */
+    int32_t qkv_dtype;   /* xlstm_dtype_t of q, k, v, o and their gradients              */
+    float scale;         /* multiplies q before use; finite                              */
+} xlstm_linattn_desc_t;
+
+/* Workspace bytes of the forward and the backward call (>= 256; 256-byte aligned
+ * memory); 0 for a NULL or invalid desc. */
+XLSTM_API size_t xlstm_linattn_workspace_size(const xlstm_linattn_desc_t *desc);
+XLSTM_API size_t xlstm_linattn_bwd_workspace_size(const xlstm_linattn_desc_t *desc);
+
+/*
+ * A whole prompt, chunked: the sequence is cut into segments, the state entering each
+ * is formed first, then all segments' outputs at once.
+ *   C_in  : initial state, or NULL (zero state)
+ *   o     : required when T > 0
+ *   C_out : final state, or NULL (not written); must not overlap C_in
+ */
+XLSTM_API xlstm_status_t xlstm_linattn_fwd(
+    const xlstm_linattn_desc_t *desc, const void *q, const void *k, const void *v,
+    const float *log_decay, const int32_t *lens, const float *C_in, void *o, float *C_out,
+    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token per sequence: q, k [B][H][d_qk], v, o [B][H][d_v]; C is read and C_new
+ * written once.  C_new may equal C exactly (in place); any other overlap is refused.
+ */
+XLSTM_API xlstm_status_t xlstm_linattn_step(
+    const xlstm_linattn_desc_t *desc, const void *q, const void *k, const void *v,
+    const float *log_decay, const float *C, void *o, float *C_new, cudaStream_t stream);
+
+/*
+ * Gradients of xlstm_linattn_fwd: do is the gradient of o, dC_out that of the final
+ * state (NULL: zero).  dq, dk, dv are written in qkv_dtype; dC_in, the gradient of the
+ * initial state (also where C_in is NULL), is fp32 and may be NULL.
+ */
+XLSTM_API xlstm_status_t xlstm_linattn_bwd(
+    const xlstm_linattn_desc_t *desc, const void *q, const void *k, const void *v,
+    const float *log_decay, const int32_t *lens, const float *C_in, const void *do_,
+    const float *dC_out, void *dq, void *dk, void *dv, float *dC_in,
+    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * ---- group norm with an activation, channels last --------------------------------
+ *
+ * Each group's D channels of each token are normalised on their own (a group is a head
+ * of a cell's output; no statistic crosses tokens), then
+ *   z = (x - mean) / sqrt(var + eps) * weight + bias     (var: biased)
+ *   y = z * act(gate)    with a gate,      y = act(z)    without
+ * y is channels last, [B][T][G * D], the order that a following projection reads; x is
+ * taken as a cell writes it (heads major) or channels last.
+ *   x, dx             x_dtype; [B][G][T][D] (XLSTM_HEADS_MAJOR) or [B][T][G][D]
+ *                     (XLSTM_CHANNELS_LAST)
+ *   y, gate, dy, dgate [B][T][G * D], y_dtype
+ *   weight, bias      [G * D] fp32, each may be NULL (1 and 0)
+ * Statistics, sums and gradients of weight and bias are fp32; 16-byte alignment for
+ * every pointer.
+ */
+typedef enum { XLSTM_HEADS_MAJOR = 0, XLSTM_CHANNELS_LAST = 1 } xlstm_layout_t;
+typedef enum { XLSTM_ACT_NONE = 0, XLSTM_ACT_SILU = 1, XLSTM_ACT_SIGMOID = 2 } xlstm_act_t;
+
+typedef struct {
+    int32_t B, T;        /* batch >= 1, tokens >= 0; B * T * G at most 2^30          */
+    int32_t G, D;        /* groups >= 1; channels of a group: a multiple of 16 in [16, 512];
+                            G * D at most 2^30                                       */
+    int32_t x_dtype, y_dtype;   /* xlstm_dtype_t                                     */
+    int32_t x_layout;    /* xlstm_layout_t                                           */
+    int32_t act;         /* xlstm_act_t                                              */
+    float eps;           /* > 0                                                      */
+} xlstm_group_norm_desc_t;
+
+XLSTM_API xlstm_status_t xlstm_group_norm(
+    const xlstm_group_norm_desc_t *desc, const void *x, const float *weight, const float *bias,
+    const void *gate, void *y, cudaStream_t stream);
+
+/*
+ * Gradients: dy is that of y.  dx is required; dgate is required with a gate and must be
+ * NULL without one; dweight and dbias ([G * D] fp32) may each be NULL, and may be asked
+ * for where weight or bias is NULL.  The statistics are formed again from x.  The sums
+ * over tokens run in a fixed order (the same inputs give the same bits).
+ *   workspace: >= xlstm_group_norm_bwd_workspace_size(desc) bytes, 256-byte aligned; not
+ *   needed (NULL) where dweight and dbias are both NULL.  It has no status block.
+ */
+XLSTM_API size_t xlstm_group_norm_bwd_workspace_size(const xlstm_group_norm_desc_t *desc);
+XLSTM_API xlstm_status_t xlstm_group_norm_bwd(
+    const xlstm_group_norm_desc_t *desc, const void *x, const float *weight, const float *bias,
+    const void *gate, const void *dy, void *dx, void *dgate, float *dweight, float *dbias,
+    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* XLSTM_LAYER_H */

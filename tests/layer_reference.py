@@ -1,0 +1,117 @@
+"""Plain 64-bit references of the layer operators, and the magnitudes that their rounding bounds are stated in.
+
+Linear attention is evaluated one token at a time, straight from C_t = l C_{t-1} + v_t k_t^T, o_t = scale C_t q_t and
+from the adjoint recurrence.  Run on absolute values, the same recurrence gives for every output the sum of the
+magnitudes of the products it consists of: an evaluation in which every product and sum carries a relative error of
+at most u is off by at most u times that sum per rounding on its path.
+"""
+import torch
+
+
+def powers(log_decay):
+    return torch.exp(log_decay.double().clamp(max=0.0))
+
+
+def fwd(q, k, v, log_decay, C0=None, lens=None, scale=1.0):
+    """(o, C_T) in float64; o is zero behind lens."""
+    q, k, v = q.double(), k.double(), v.double()
+    B, H, T, dqk = q.shape
+    dv = v.shape[-1]
+    l = powers(log_decay).to(q.device)[None, :, None, None]
+    C = torch.zeros(B, H, dv, dqk, dtype=torch.float64, device=q.device) if C0 is None else C0.double().clone()
+    lens = torch.full((B,), T) if lens is None else lens.cpu().clamp(0, T)
+    o = torch.zeros(B, H, T, dv, dtype=torch.float64, device=q.device)
+    for t in range(T):
+        on = [b for b in range(B) if t < int(lens[b])]
+        if not on:
+            break
+        C[on] = l * C[on] + v[on, :, t, :, None] * k[on, :, t, None, :]
+        o[on, :, t] = scale * (C[on] @ q[on, :, t, :, None])[..., 0]
+    return o, C
+
+
+def bwd(q, k, v, log_decay, do, C0=None, dCT=None, lens=None, scale=1.0):
+    """dict(dq, dk, dv, dC0) in float64; zero behind lens."""
+    q, k, v, do = q.double(), k.double(), v.double(), do.double()
+    B, H, T, dqk = q.shape
+    dv = v.shape[-1]
+    l = powers(log_decay).to(q.device)[None, :, None, None]
+    zero = lambda: torch.zeros(B, H, dv, dqk, dtype=torch.float64, device=q.device)  # noqa: E731
+    C = zero() if C0 is None else C0.double().clone()
+    E = zero() if dCT is None else dCT.double().clone()
+    lens = torch.full((B,), T) if lens is None else lens.cpu().clamp(0, T)
+    g = dict(dq=torch.zeros_like(q), dk=torch.zeros_like(k), dv=torch.zeros_like(v))
+    live = [[b for b in range(B) if t < int(lens[b])] for t in range(T)]
+    for t in range(T):
+        on = live[t]
+        if on:
+            C[on] = l * C[on] + v[on, :, t, :, None] * k[on, :, t, None, :]
+            g["dq"][on, :, t] = scale * (C[on].transpose(-1, -2) @ do[on, :, t, :, None])[..., 0]
+    for t in reversed(range(T)):
+        on = live[t]
+        if on:
+            E[on] = E[on] + scale * do[on, :, t, :, None] * q[on, :, t, None, :]   # gradient of C_t
+            g["dk"][on, :, t] = (E[on].transpose(-1, -2) @ v[on, :, t, :, None])[..., 0]
+            g["dv"][on, :, t] = (E[on] @ k[on, :, t, :, None])[..., 0]
+            E[on] = l * E[on]
+    return dict(g, dC0=E)
+
+
+def _abs(*xs):
+    return [None if x is None else x.double().abs() for x in xs]
+
+
+def fwd_magnitude(q, k, v, log_decay, C0=None, lens=None, scale=1.0):
+    q, k, v, C0 = _abs(q, k, v, C0)
+    return fwd(q, k, v, log_decay, C0, lens, abs(scale))
+
+
+def bwd_magnitude(q, k, v, log_decay, do, C0=None, dCT=None, lens=None, scale=1.0):
+    q, k, v, do, C0, dCT = _abs(q, k, v, do, C0, dCT)
+    return bwd(q, k, v, log_decay, do, C0, dCT, lens, abs(scale))
+
+
+def sum_roundings(T, d):
+    """Roundings on the path of one output of fp32 products: the sums over at most `d` channels, one segment's tokens
+    (128 to 512) and the segments before it, and 32 for the weights, the products and the last operations.  Tensor-core
+    sums may truncate: one step each, where a rounding is half a step."""
+    return d + min(T, 512) + T // 128 + 32
+
+
+def output_bound(ref, mag, T, d, dtype):
+    """Bound on |o - ref| (and on the gradients of q, k, v).
+
+    fp32 inputs: roundings of half a step 2^-24 each, on the sum of magnitudes.
+    bf16 inputs: the weighted scores and the entering state are one bf16 copy each (half a step 2^-8 of the part they
+    make), the state's own terms are bf16 pairs (2^-16), the sums fp32 (2^-23 a step), and the result is rounded once
+    (2^-8 of itself, plus the part of its error)."""
+    if dtype == torch.float32:
+        return sum_roundings(T, d) * 2.0 ** -24 * mag
+    before = (2.0 ** -8 + 2.0 ** -16 + sum_roundings(T, d) * 2.0 ** -23) * mag
+    return before + 2.0 ** -8 * (ref.abs() + before)
+
+
+def state_bound(mag, T, d, dtype):
+    """Bound on the fp32 final state (and its gradient): bf16 inputs enter as pairs, whose second rounding leaves
+    2^-16 of a term."""
+    u = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -23
+    return (sum_roundings(T, d) * u + (0.0 if dtype == torch.float32 else 2.0 ** -16)) * mag
+
+
+# ---- group norm ---------------------------------------------------------------------------------------------
+def act(x, name):
+    return {"none": x, "sigmoid": torch.sigmoid(x), "silu": x * torch.sigmoid(x)}[name]
+
+
+def group_norm(x, weight, bias, gate, name, layout, eps):
+    """y [B,T,G*D] in float64 (differentiable)."""
+    x = x.double()
+    x = x.transpose(1, 2) if layout == "heads" else x
+    mu = x.mean(-1, keepdim=True)
+    var = ((x - mu) ** 2).mean(-1, keepdim=True)
+    z = ((x - mu) / torch.sqrt(var + eps)).flatten(2)
+    if weight is not None:
+        z = z * weight.double()
+    if bias is not None:
+        z = z + bias.double()
+    return act(z, name) if gate is None else z * act(gate.double(), name)

@@ -1,0 +1,205 @@
+"""Host-side checks of the layer operators (no GPU, no kernel launched): refusals, sizes, and the references
+themselves against gradients by differences."""
+import os
+
+import pytest
+import torch
+
+import layer_reference as ref
+from xlstm_mlstm_matrix_b200 import capi
+
+INVALID, UNSUPPORTED, WORKSPACE = capi.XLSTM_ERR_INVALID_ARG, capi.XLSTM_ERR_UNSUPPORTED, capi.XLSTM_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(capi.LIB_PATH):
+        from xlstm_mlstm_matrix_b200 import build
+        build.build()
+    return capi.load()
+
+
+A = {n: (i + 1) << 24 for i, n in enumerate(("q", "k", "v", "ld", "lens", "C0", "o", "C1", "do", "dC1", "dq", "dk", "dv",
+                                             "dC0", "ws"))}
+
+
+def fwd(desc, **over):
+    a = dict(A, lens=None, C0=None, wsb=1 << 40, **{k: v for k, v in over.items() if k in ()})
+    a.update(over)
+    return capi.xlstm_linattn_fwd(desc, a["q"], a["k"], a["v"], a["ld"], a["lens"], a["C0"], a["o"], a["C1"], a["ws"],
+                                  a["wsb"])
+
+
+def step(desc, **over):
+    a = dict(A, **over)
+    return capi.xlstm_linattn_step(desc, a["q"], a["k"], a["v"], a["ld"], a["C0"], a["o"], a["C1"])
+
+
+def bwd(desc, **over):
+    a = dict(A, lens=None, C0=None, dC1=None, wsb=1 << 40)
+    a.update(over)
+    return capi.xlstm_linattn_bwd(desc, a["q"], a["k"], a["v"], a["ld"], a["lens"], a["C0"], a["do"], a["dC1"], a["dq"],
+                                  a["dk"], a["dv"], a["dC0"], a["ws"], a["wsb"])
+
+
+SMALL = dict(B=2, H=2, T=70, d_qk=32, d_v=48)
+
+
+@pytest.mark.parametrize("field,value", [("B", 0), ("H", -1), ("T", -1), ("d_qk", 8), ("d_qk", 528), ("d_v", 24),
+                                         ("d_v", 0), ("qkv_dtype", 2), ("scale", float("nan")), ("scale", float("inf")),
+                                         ("T", (1 << 30) + 1), ("B", 1 << 25)])
+def test_linattn_bad_descs(field, value):
+    d = capi.make_linattn_desc(**SMALL)
+    setattr(d, field, value)
+    assert fwd(d) == INVALID and bwd(d) == INVALID
+    assert capi.xlstm_linattn_workspace_size(d) == 0 and capi.xlstm_linattn_bwd_workspace_size(d) == 0
+    if field != "T" and value != 1 << 25:   # the step call ignores T
+        assert step(d) == INVALID
+
+
+def test_linattn_pointers():
+    d = capi.make_linattn_desc(**SMALL)
+    for n in ("q", "k", "v", "ld", "o"):
+        assert fwd(d, **{n: None}) == INVALID, n
+    for n in ("q", "k", "v", "C0", "o", "C1"):
+        assert fwd(d, **{n: A[n] + 8}) == INVALID, n
+    for n in ("ld", "lens"):
+        assert fwd(d, **{n: A[n] + 2}) == INVALID, n
+    for n in ("q", "k", "v", "ld", "C0", "o", "C1"):
+        assert step(d, **{n: None}) == INVALID, n
+        assert step(d, **{n: A[n] + 2}) == INVALID, n
+    for n in ("q", "k", "v", "ld", "do", "dq", "dk", "dv"):
+        assert bwd(d, **{n: None}) == INVALID, n
+    for n in ("q", "do", "dC1", "C0", "dq", "dk", "dv", "dC0"):
+        assert bwd(d, **{n: A[n] + 4}) == INVALID, n
+    assert capi.load().xlstm_linattn_fwd(None, *[None] * 8, None, 0, None) == INVALID
+
+
+def test_linattn_overlaps():
+    d = capi.make_linattn_desc(**SMALL)
+    n_v, n_C = 2 * 2 * 70 * 48 * 2, 2 * 2 * 32 * 48 * 4
+    assert fwd(d, o=A["q"]) == INVALID
+    assert fwd(d, o=A["v"] + n_v - 16) == INVALID
+    assert fwd(d, C0=A["C0"], C1=A["C0"]) == INVALID
+    assert fwd(d, C1=A["o"] + 16) == INVALID
+    assert fwd(d, lens=A["o"] + 16) == INVALID
+    assert fwd(d, ws=A["q"] // 256 * 256) == INVALID
+    assert step(d, C1=A["C0"] + 256) == INVALID            # in place is exact or not at all
+    assert step(d, o=A["C0"] + n_C - 16) == INVALID
+    assert bwd(d, dq=A["q"]) == INVALID
+    assert bwd(d, dk=A["dv"]) == INVALID
+    assert bwd(d, dC1=A["dC0"]) == INVALID
+
+
+def test_linattn_workspace():
+    for dt in (capi.XLSTM_F32, capi.XLSTM_BF16):
+        d = capi.make_linattn_desc(**SMALL, dtype=dt)
+        need, needb = capi.xlstm_linattn_workspace_size(d), capi.xlstm_linattn_bwd_workspace_size(d)
+        assert 256 <= need <= needb
+        assert fwd(d, ws=None) == WORKSPACE and fwd(d, wsb=need - 1) == WORKSPACE and fwd(d, ws=A["ws"] + 16) == INVALID
+        assert bwd(d, ws=None) == WORKSPACE and bwd(d, wsb=needb - 1) == WORKSPACE and bwd(d, ws=A["ws"] + 16) == INVALID
+        d.T = 0
+        assert capi.xlstm_linattn_workspace_size(d) >= 256
+
+
+N = dict(x=1 << 24, w=2 << 24, b=3 << 24, g=4 << 24, y=5 << 24, dy=6 << 24, dx=7 << 24, dg=8 << 24, dw=9 << 24,
+         db=10 << 24, ws=11 << 24)
+
+
+def norm(desc, **over):
+    a = dict(N, **over)
+    return capi.xlstm_group_norm(desc, a["x"], a["w"], a["b"], a["g"], a["y"])
+
+
+def norm_bwd(desc, **over):
+    a = dict(N, wsb=1 << 40)
+    a.update(over)
+    return capi.xlstm_group_norm_bwd(desc, a["x"], a["w"], a["b"], a["g"], a["dy"], a["dx"], a["dg"], a["dw"], a["db"],
+                                     a["ws"], a["wsb"])
+
+
+@pytest.mark.parametrize("field,value", [("B", 0), ("T", -1), ("G", 0), ("D", 8), ("D", 40), ("D", 528), ("x_dtype", 2),
+                                         ("y_dtype", -1), ("x_layout", 2), ("act", 3), ("act", -1), ("eps", 0.0),
+                                         ("eps", float("inf")), ("eps", float("nan")), ("T", 1 << 30), ("G", 1 << 27)])
+def test_group_norm_bad_descs(field, value):
+    d = capi.make_group_norm_desc(2, 5, 3, 32)
+    setattr(d, field, value)
+    assert norm(d) == INVALID and norm_bwd(d) == INVALID
+    assert capi.xlstm_group_norm_bwd_workspace_size(d) == 0
+
+
+def test_group_norm_pointers_and_overlaps():
+    d = capi.make_group_norm_desc(2, 5, 3, 32)
+    n = 2 * 5 * 3 * 32 * 2
+    for k in ("x", "y"):
+        assert norm(d, **{k: None}) == INVALID, k
+    for k in ("x", "w", "b", "g", "y"):
+        assert norm(d, **{k: N[k] + 4}) == INVALID, k
+    assert norm(d, y=N["x"]) == INVALID and norm(d, y=N["g"] + n - 16) == INVALID and norm(d, y=N["w"]) == INVALID
+    for k in ("x", "dy", "dx"):
+        assert norm_bwd(d, **{k: None}) == INVALID, k
+    assert norm_bwd(d, dg=None) == INVALID and norm_bwd(d, g=None) == INVALID   # dgate exactly with a gate
+    assert norm_bwd(d, dx=N["dy"]) == INVALID and norm_bwd(d, dw=N["db"]) == INVALID
+    assert norm_bwd(d, dx=N["dg"]) == INVALID
+    need = capi.xlstm_group_norm_bwd_workspace_size(d)
+    assert need >= 256
+    assert norm_bwd(d, ws=None) == WORKSPACE and norm_bwd(d, wsb=need - 1) == WORKSPACE
+    assert norm_bwd(d, ws=N["ws"] + 16) == INVALID
+    assert capi.xlstm_group_norm(capi.make_group_norm_desc(2, 0, 3, 32), None, None, None, None, None) == capi.XLSTM_OK
+
+
+def test_python_helpers_refuse():
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)  # noqa: E731
+    q, ld = z(1, 2, 4, 16), z(2)
+    with pytest.raises(ValueError, match="CUDA"):
+        capi.linattn_fwd(q, q, q, ld)
+    with pytest.raises(TypeError):
+        capi.linattn_fwd(q.half(), q.half(), q.half(), ld)
+    with pytest.raises(TypeError):
+        capi.linattn_fwd(q, q.bfloat16(), q, ld)
+    with pytest.raises(ValueError, match="k: shape"):
+        capi.linattn_fwd(q, z(1, 2, 5, 16), q, ld)
+    with pytest.raises(ValueError, match="contiguous"):
+        capi.linattn_fwd(q, z(1, 4, 2, 16).transpose(1, 2), q, ld)
+    with pytest.raises(ValueError, match="log_decay"):
+        capi.linattn_fwd(q, q, q, z(3))
+    with pytest.raises(TypeError, match="lens"):
+        capi.linattn_fwd(q, q, q, ld, lens=torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError, match="state"):
+        capi.linattn_fwd(q, q, q, ld, state=z(1, 2, 16, 8))
+    with pytest.raises(ValueError, match="axes"):
+        capi.linattn_step(q, q, q, ld, z(1, 2, 16, 16))
+    with pytest.raises(ValueError, match="do"):
+        capi.linattn_bwd(q, q, q, ld, z(1, 2, 3, 16))
+    x = z(1, 2, 4, 16)
+    for kw in (dict(layout="nchw"), dict(act="relu"), dict(weight=z(31)), dict(gate=z(1, 4, 31)),
+               dict(gate=z(1, 4, 32), out_dtype=torch.bfloat16), dict(out_dtype=torch.float16)):
+        with pytest.raises((ValueError, TypeError)):
+            capi.group_norm(x, **kw)
+    with pytest.raises(ValueError, match="dy"):
+        capi.group_norm_bwd(z(1, 2, 32), x)
+
+
+# ---- the references: gradients by differences --------------------------------------------------------------
+def test_reference_gradients_against_differences():
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    B, H, T, dk, dv = 2, 2, 5, 3, 4
+    lens = torch.tensor([5, 3], dtype=torch.int32)
+    ld = torch.tensor([-0.3, -2.0], dtype=torch.float64)
+    ins = dict(q=r(B, H, T, dk), k=r(B, H, T, dk), v=r(B, H, T, dv), C0=r(B, H, dv, dk))
+    do, dC = r(B, H, T, dv), r(B, H, dv, dk)
+
+    def loss(x):
+        o, C = ref.fwd(x["q"], x["k"], x["v"], ld, x["C0"], lens, 0.7)
+        return float((o * do).sum() + (C * dC).sum())
+    got = ref.bwd(ins["q"], ins["k"], ins["v"], ld, do, ins["C0"], dC, lens, 0.7)
+    for name, gname in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("C0", "dC0")):
+        x = ins[name]
+        for i in range(x.numel()):
+            h = 1e-6
+            up, down = x.clone(), x.clone()
+            up.view(-1)[i] += h
+            down.view(-1)[i] -= h
+            num = (loss(dict(ins, **{name: up})) - loss(dict(ins, **{name: down}))) / (2 * h)
+            assert abs(num - float(got[gname].reshape(-1)[i])) < 1e-6, (name, i)

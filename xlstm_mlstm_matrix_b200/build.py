@@ -46,7 +46,8 @@ def _deps_hash(src: str, flags) -> str:
     for f in sorted(os.listdir(CSRC)):
         if f.endswith((".cuh", ".h")):
             h.update(open(os.path.join(CSRC, f), "rb").read())
-    h.update(open(os.path.join(INCLUDE, "xlstm_mlstm.h"), "rb").read())
+    for f in sorted(os.listdir(INCLUDE)):
+        h.update(open(os.path.join(INCLUDE, f), "rb").read())
     return h.hexdigest()[:16]
 
 

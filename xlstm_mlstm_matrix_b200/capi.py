@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in ``include/xlstm_mlstm.h``.
+"""ctypes binding of the C ABI in ``include/xlstm_mlstm.h`` and ``include/xlstm_layer.h``.
 
 The functions named ``xlstm_*`` mirror the C entry points one to one: they take
 plain integers (device addresses) or objects with ``data_ptr()`` (torch tensors)
@@ -17,13 +17,18 @@ LIB_PATH = os.path.join(HERE, "libxlstm_mlstm.so")
 XLSTM_OK, XLSTM_ERR_INVALID_ARG, XLSTM_ERR_UNSUPPORTED = 0, 1, 2
 XLSTM_ERR_CUDA, XLSTM_ERR_TIMEOUT, XLSTM_ERR_WORKSPACE = 3, 4, 5
 XLSTM_F32, XLSTM_BF16 = 0, 1
+XLSTM_HEADS_MAJOR, XLSTM_CHANNELS_LAST = 0, 1
+XLSTM_ACT_NONE, XLSTM_ACT_SILU, XLSTM_ACT_SIGMOID = 0, 1, 2
 
 EXPORTED = ("xlstm_mlstm_fwd_chunkwise", "xlstm_mlstm_fwd_recurrent", "xlstm_mlstm_step",
             "xlstm_mlstm_workspace_size", "xlstm_mlstm_workspace_status", "xlstm_status_string",
             "xlstm_mlstm_version", "xlstm_mlstm_chunkwise_kernel", "xlstm_mlstm_test_timeout_next",
             "xlstm_mlstm_fwd_chunkwise_noalloc", "xlstm_mlstm_workspace_size_parallel",
             "xlstm_mlstm_fwd_chunkwise_out", "xlstm_mlstm_noalloc_status", "xlstm_mlstm_segment_summary",
-            "xlstm_mlstm_combine_states", "xlstm_mlstm_bwd_chunkwise", "xlstm_mlstm_bwd_workspace_size")
+            "xlstm_mlstm_combine_states", "xlstm_mlstm_bwd_chunkwise", "xlstm_mlstm_bwd_workspace_size",
+            "xlstm_linattn_fwd", "xlstm_linattn_step", "xlstm_linattn_bwd", "xlstm_linattn_workspace_size",
+            "xlstm_linattn_bwd_workspace_size", "xlstm_group_norm", "xlstm_group_norm_bwd",
+            "xlstm_group_norm_bwd_workspace_size")
 
 
 class xlstm_mlstm_desc_t(ctypes.Structure):
@@ -34,6 +39,18 @@ class xlstm_mlstm_desc_t(ctypes.Structure):
 
 class xlstm_mlstm_output_t(ctypes.Structure):
     _fields_ = [("o_pre", ctypes.c_void_p), ("o_dtype", ctypes.c_int32), ("h_dtype", ctypes.c_int32)]
+
+
+class xlstm_linattn_desc_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("d_qk", ctypes.c_int32), ("d_v", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class xlstm_group_norm_desc_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("G", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("x_layout", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class XlstmError(RuntimeError):
@@ -89,6 +106,19 @@ def load(path: str = LIB_PATH):
     lib.xlstm_mlstm_chunkwise_kernel.restype = ctypes.c_char_p
     lib.xlstm_mlstm_test_timeout_next.argtypes = [ctypes.c_int32]
     lib.xlstm_mlstm_test_timeout_next.restype = None
+    lp, gp = ctypes.POINTER(xlstm_linattn_desc_t), ctypes.POINTER(xlstm_group_norm_desc_t)
+    lib.xlstm_linattn_fwd.argtypes = [lp] + [vp] * 8 + [vp, sz, vp]
+    lib.xlstm_linattn_step.argtypes = [lp] + [vp] * 7 + [vp]
+    lib.xlstm_linattn_bwd.argtypes = [lp] + [vp] * 12 + [vp, sz, vp]
+    lib.xlstm_group_norm.argtypes = [gp] + [vp] * 5 + [vp]
+    lib.xlstm_group_norm_bwd.argtypes = [gp] + [vp] * 9 + [vp, sz, vp]
+    for name in ("xlstm_linattn_fwd", "xlstm_linattn_step", "xlstm_linattn_bwd", "xlstm_group_norm",
+                 "xlstm_group_norm_bwd"):
+        getattr(lib, name).restype = st
+    for name, p in (("xlstm_linattn_workspace_size", lp), ("xlstm_linattn_bwd_workspace_size", lp),
+                    ("xlstm_group_norm_bwd_workspace_size", gp)):
+        getattr(lib, name).argtypes = [p]
+        getattr(lib, name).restype = sz
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -218,6 +248,56 @@ def xlstm_mlstm_chunkwise_kernel(desc) -> str:
 
 def xlstm_mlstm_test_timeout_next(enable: int = 1) -> None:
     load().xlstm_mlstm_test_timeout_next(int(enable))
+
+
+# ---- xlstm_layer.h: one-to-one C entry points -------------------------------------
+def make_linattn_desc(B, H, T, d_qk, d_v, dtype=XLSTM_BF16, scale=1.0) -> xlstm_linattn_desc_t:
+    return xlstm_linattn_desc_t(B, H, T, d_qk, d_v, dtype, scale)
+
+
+def make_group_norm_desc(B, T, G, D, x_dtype=XLSTM_BF16, y_dtype=XLSTM_BF16, x_layout=XLSTM_HEADS_MAJOR,
+                         act=XLSTM_ACT_SILU, eps=1e-5) -> xlstm_group_norm_desc_t:
+    return xlstm_group_norm_desc_t(B, T, G, D, x_dtype, y_dtype, x_layout, act, eps)
+
+
+def xlstm_linattn_workspace_size(desc) -> int:
+    return int(load().xlstm_linattn_workspace_size(ctypes.byref(desc)))
+
+
+def xlstm_linattn_bwd_workspace_size(desc) -> int:
+    return int(load().xlstm_linattn_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def xlstm_linattn_fwd(desc, q, k, v, log_decay, lens, C_in, o, C_out, workspace, workspace_bytes, stream=None) -> int:
+    return load().xlstm_linattn_fwd(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(log_decay), _p(lens), _p(C_in), _p(o),
+                                    _p(C_out), _p(workspace), int(workspace_bytes), _s(stream))
+
+
+def xlstm_linattn_step(desc, q, k, v, log_decay, C, o, C_new, stream=None) -> int:
+    return load().xlstm_linattn_step(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(log_decay), _p(C), _p(o), _p(C_new),
+                                     _s(stream))
+
+
+def xlstm_linattn_bwd(desc, q, k, v, log_decay, lens, C_in, do, dC_out, dq, dk, dv, dC_in, workspace, workspace_bytes,
+                      stream=None) -> int:
+    return load().xlstm_linattn_bwd(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(log_decay), _p(lens), _p(C_in), _p(do),
+                                    _p(dC_out), _p(dq), _p(dk), _p(dv), _p(dC_in), _p(workspace), int(workspace_bytes),
+                                    _s(stream))
+
+
+def xlstm_group_norm(desc, x, weight, bias, gate, y, stream=None) -> int:
+    return load().xlstm_group_norm(ctypes.byref(desc), _p(x), _p(weight), _p(bias), _p(gate), _p(y), _s(stream))
+
+
+def xlstm_group_norm_bwd_workspace_size(desc) -> int:
+    return int(load().xlstm_group_norm_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def xlstm_group_norm_bwd(desc, x, weight, bias, gate, dy, dx, dgate, dweight, dbias, workspace, workspace_bytes,
+                         stream=None) -> int:
+    return load().xlstm_group_norm_bwd(ctypes.byref(desc), _p(x), _p(weight), _p(bias), _p(gate), _p(dy), _p(dx),
+                                       _p(dgate), _p(dweight), _p(dbias), _p(workspace), int(workspace_bytes),
+                                       _s(stream))
 
 
 def status_string(status: int) -> str:
@@ -374,4 +454,179 @@ def bwd(q, k, v, i_pre, f_pre, dh, state=None, dstate=None, qk_scale=None, strea
     check(xlstm_mlstm_bwd_chunkwise(desc, q, k, v, i_pre, f_pre, C0, n0, m0, dh, dC, dn, g["dq"], g["dk"],
                                     g["dv"], g["di"], g["df"], g["dC0"], g["dn0"], g["dm0"], workspace,
                                     workspace.numel(), stream), "xlstm_mlstm_bwd_chunkwise")
+    return g
+
+
+# ---- xlstm_layer.h: torch conveniences (checks, allocation, marshalling) ------------
+def _want(x, name, shape, dtypes, device):
+    """x is a contiguous tensor of this shape, on this device, of one of these dtypes."""
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {x.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _call_on(device, stream):
+    """The device's context and the stream to launch on (the device's current one by default)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors expected, got {device}")
+    return torch.cuda.device(device), stream if stream is not None else torch.cuda.current_stream(device)
+
+
+def _linattn_inputs(q, k, v, log_decay, state, lens, token_axis):
+    import torch
+    _dtype_code(q)
+    dev, f32 = q.device, (torch.float32,)
+    if q.dim() != 3 + token_axis:
+        raise ValueError(f"q: {q.dim()} axes, expected {3 + token_axis}")
+    B, H, dqk, dv = q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]
+    T = q.shape[2] if token_axis else 1
+    _want(q, "q", q.shape, (q.dtype,), dev)
+    _want(k, "k", q.shape, (q.dtype,), dev)
+    _want(v, "v", (*q.shape[:-1], dv), (q.dtype,), dev)
+    _want(log_decay, "log_decay", (H,), f32, dev)
+    if state is not None:
+        _want(state, "state", (B, H, dv, dqk), f32, dev)
+    if lens is not None:
+        _want(lens, "lens", (B,), (torch.int32,), dev)
+    return B, H, T, dqk, dv
+
+
+def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=None, workspace=None, out=None):
+    """Linear attention with a decay per head over whole prompts, through xlstm_linattn_fwd:
+    C_t = exp(log_decay[h]) C_{t-1} + v_t k_t^T, o_t = scale C_t q_t.
+
+    q, k [B,H,T,dqk], v [B,H,T,dv] (bf16 or fp32), log_decay [H] fp32 (<= 0), state [B,H,dv,dqk] fp32 or None
+    (zero), lens [B] int32 or None (padded batch: sequence b has lens[b] tokens, o is zero behind them); scale
+    defaults to dqk ** -0.5.  Returns (o, C): o [B,H,T,dv] in q's type and the final state.
+    out: (o, C) to write into; C may be None (not formed)."""
+    import torch
+    B, H, T, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, lens, 1)
+    dev = q.device
+    desc = make_linattn_desc(B, H, T, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
+    ctx, stream = _call_on(dev, stream)
+    if out is None:
+        o, C = torch.empty_like(v), torch.empty(B, H, dv, dqk, device=dev, dtype=torch.float32)
+    else:
+        o, C = out
+        _want(o, "out[0]", v.shape, (v.dtype,), dev)
+        if C is not None:
+            _want(C, "out[1]", (B, H, dv, dqk), (torch.float32,), dev)
+    with ctx:
+        if workspace is None:
+            workspace = torch.empty(max(256, xlstm_linattn_workspace_size(desc)), device=dev, dtype=torch.uint8)
+        check(xlstm_linattn_fwd(desc, q, k, v, log_decay, lens, state, o, C, workspace, workspace.numel(), stream),
+              "xlstm_linattn_fwd")
+    return o, C
+
+
+def linattn_step(q, k, v, log_decay, state, scale=None, stream=None, out=None, inplace=False):
+    """One token per sequence through xlstm_linattn_step.  q, k [B,H,dqk], v [B,H,dv], state [B,H,dv,dqk].
+    Returns (o, C'); inplace=True updates state itself.  out: (o, C') to write into."""
+    import torch
+    B, H, _, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, None, 0)
+    desc = make_linattn_desc(B, H, 1, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
+    ctx, stream = _call_on(q.device, stream)
+    if out is None:
+        o, C = torch.empty_like(v), state if inplace else torch.empty_like(state)
+    else:
+        o, C = out[0], state if inplace else out[1]
+        _want(o, "out[0]", v.shape, (v.dtype,), q.device)
+        _want(C, "out[1]", state.shape, (torch.float32,), q.device)
+    with ctx:
+        check(xlstm_linattn_step(desc, q, k, v, log_decay, state, o, C, stream), "xlstm_linattn_step")
+    return o, C
+
+
+def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lens=None, scale=None, stream=None, workspace=None):
+    """Gradients of linattn_fwd through xlstm_linattn_bwd: do is the gradient of o (q's type), dstate that of the
+    final state (fp32) or None.  Returns dict(dq, dk, dv, dC0): the inputs' types, dC0 fp32."""
+    import torch
+    B, H, T, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, lens, 1)
+    dev = q.device
+    _want(do, "do", v.shape, (v.dtype,), dev)
+    if dstate is not None:
+        _want(dstate, "dstate", (B, H, dv, dqk), (torch.float32,), dev)
+    desc = make_linattn_desc(B, H, T, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
+    ctx, stream = _call_on(dev, stream)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             dC0=torch.empty(B, H, dv, dqk, device=dev, dtype=torch.float32))
+    with ctx:
+        if workspace is None:
+            workspace = torch.empty(max(256, xlstm_linattn_bwd_workspace_size(desc)), device=dev, dtype=torch.uint8)
+        check(xlstm_linattn_bwd(desc, q, k, v, log_decay, lens, state, do, dstate, g["dq"], g["dk"], g["dv"], g["dC0"],
+                                workspace, workspace.numel(), stream), "xlstm_linattn_bwd")
+    return g
+
+
+_LAYOUTS = {"heads": XLSTM_HEADS_MAJOR, "tokens": XLSTM_CHANNELS_LAST}
+_ACTS = {"none": XLSTM_ACT_NONE, "silu": XLSTM_ACT_SILU, "sigmoid": XLSTM_ACT_SIGMOID}
+
+
+def _group_norm_inputs(x, weight, bias, gate, act, layout, eps, y_dtype):
+    import torch
+    if layout not in _LAYOUTS or act not in _ACTS:
+        raise ValueError(f"layout {layout!r} (of {sorted(_LAYOUTS)}), act {act!r} (of {sorted(_ACTS)})")
+    both = (torch.float32, torch.bfloat16)
+    if x.dim() != 4:
+        raise ValueError(f"x: {x.dim()} axes, expected 4")
+    B, G, T, D = x.shape if layout == "heads" else (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
+    _want(x, "x", x.shape, both, x.device)
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is not None:
+            _want(p, name, (G * D,), (torch.float32,), x.device)
+    if y_dtype not in both:
+        raise TypeError(f"y must be bf16 or fp32, got {y_dtype}")
+    if gate is not None:
+        _want(gate, "gate", (B, T, G * D), (y_dtype,), x.device)
+    code = {torch.float32: XLSTM_F32, torch.bfloat16: XLSTM_BF16}
+    desc = make_group_norm_desc(B, T, G, D, code[x.dtype], code[y_dtype], _LAYOUTS[layout], _ACTS[act], eps)
+    return desc, (B, T, G * D)
+
+
+def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads", eps=1e-5, out_dtype=None, stream=None,
+               out=None):
+    """Group norm per token and head with an activation, channels last, through xlstm_group_norm:
+    z = (x - mean) / sqrt(var + eps) weight + bias over each head's channels, then z act(gate), or act(z) without
+    a gate.
+
+    x [B,H,T,D] (layout "heads", as the cells write it) or [B,T,H,D] ("tokens"), bf16 or fp32; weight, bias [H*D]
+    fp32 or None; gate [B,T,H*D] in the output's type.  Returns y [B,T,H*D] in out_dtype (the gate's type, else
+    x's, by default)."""
+    import torch
+    dt = out.dtype if out is not None else out_dtype if out_dtype is not None else gate.dtype if gate is not None else x.dtype
+    desc, shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
+    ctx, stream = _call_on(x.device, stream)
+    if out is None:
+        out = torch.empty(shape, device=x.device, dtype=dt)
+    else:
+        _want(out, "out", shape, (dt,), x.device)
+    with ctx:
+        check(xlstm_group_norm(desc, x, weight, bias, gate, out, stream), "xlstm_group_norm")
+    return out
+
+
+def group_norm_bwd(dy, x, weight=None, bias=None, gate=None, act="silu", layout="heads", eps=1e-5, stream=None,
+                   workspace=None):
+    """Gradients of group_norm through xlstm_group_norm_bwd: dict(dx, dgate, dweight, dbias); None in the place of
+    what was not given."""
+    import torch
+    desc, shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
+    _want(dy, "dy", shape, (dy.dtype,), x.device)
+    ctx, stream = _call_on(x.device, stream)
+    g = dict(dx=torch.empty_like(x), dgate=None if gate is None else torch.empty_like(gate),
+             dweight=None if weight is None else torch.empty_like(weight),
+             dbias=None if bias is None else torch.empty_like(bias))
+    with ctx:
+        if workspace is None and (weight is not None or bias is not None):
+            workspace = torch.empty(max(256, xlstm_group_norm_bwd_workspace_size(desc)), device=x.device,
+                                    dtype=torch.uint8)
+        check(xlstm_group_norm_bwd(desc, x, weight, bias, gate, dy, g["dx"], g["dgate"], g["dweight"], g["dbias"],
+                                   workspace, 0 if workspace is None else workspace.numel(), stream),
+              "xlstm_group_norm_bwd")
     return g

@@ -3,27 +3,18 @@
 #include <cmath>
 #include <cstring>
 
+#include "arg_checks.cuh"
 #include "common.cuh"
 
 namespace {
 
 using xlstm::FwdArgs;
+using xlstm::aligned16;
+using xlstm::overlap;
+using xlstm::Range;
+using xlstm::rg;
 
 constexpr size_t kWorkspaceBytes = 256;   // status block (16 B), padded
-
-bool aligned16(const void *p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    const char *lo;
-    size_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-    if (!a.lo || !b.lo || a.bytes == 0 || b.bytes == 0) return false;
-    return a.lo < b.lo + b.bytes && b.lo < a.lo + a.bytes;
-}
-
-Range rg(const void *p, size_t bytes) { return Range{static_cast<const char *>(p), bytes}; }
 
 bool dims_ok(const xlstm_mlstm_desc_t *d) {
     if (d->B < 1 || d->H < 1 || d->T < 0) return false;

@@ -1,0 +1,89 @@
+// Internal declarations of the linear attention with a fixed decay per head.
+//
+//   C_t = l C_{t-1} + v_t k_t^T,   o_t = scale C_t q_t,   l = e^{log_decay[h]} in [0, 1]
+//
+// A prompt is cut into segments of G tokens, [s_n, e_n) with s_n = nG and e_n = min(s_n + G, len).
+// With U_n = sum_{s in n} l^{e_n-1-s} v_s k_s^T the state entering segment n obeys
+// C_{n+1} = l^{e_n-s_n} C_n + U_n, and inside a segment the unrolled recurrence is a masked product:
+//   o_t = scale sum_{s_n <= s <= t} l^{t-s} (q_t.k_s) v_s + scale l^{t-s_n+1} C_n q_t.
+// The gradients are the same two steps with other operands, dk and dv with time reversed:
+//   E_{n-1} = l^{e_n-s_n} E_n + scale sum_{t in n} l^{t-s_n+1} do_t q_t^T        (E_last = dC_T)
+//   dq_t = scale sum_{s<=t} l^{t-s} (do_t.v_s) k_s + scale l^{t-s_n+1} C_n^T do_t
+//   dk_s = scale sum_{t>=s} l^{t-s} (v_s.do_t) q_t + l^{e_n-1-s} E_n^T v_s
+//   dv_s = scale sum_{t>=s} l^{t-s} (k_s.q_t) do_t + l^{e_n-1-s} E_n k_s
+// so both steps are written once, over "queries" X, "keys" Y and "values" Z: a state step that sums
+// w_s z_s y_s^T per segment and chains the sums, and a tile step that forms the outputs of all segments at once.
+// Every power of l has an exponent >= 0, so no factor exceeds 1 whatever the decay.
+#pragma once
+#include "common.cuh"
+#include "../../include/xlstm_layer.h"
+
+namespace xlstm {
+
+struct LinAttnArgs {
+    int B, H, T, dqk, dv, dtype;
+    float scale;
+    const void *q, *k, *v;
+    const float *log_decay;      // [H]
+    const int32_t *lens;         // [B] or null (every sequence has T tokens)
+    const float *C0;             // [B][H][dv][dqk] or null (zero)
+    void *o;                     // forward output
+    float *C1;                   // final state or null
+    const void *do_;             // backward: upstream gradient of o
+    const float *dC1;            // ... of the final state, or null (zero)
+    void *dq, *dk, *dv_;
+    float *dC0;                  // gradient of the initial state, or null
+    void *workspace;             // behind the status block
+    int32_t *status;             // device status block
+};
+
+size_t linattn_workspace_bytes(const LinAttnArgs &a, bool backward);   // without the status block
+cudaError_t launch_linattn_fwd(const LinAttnArgs &a, cudaStream_t s);
+cudaError_t launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t s);
+cudaError_t launch_linattn_step(const LinAttnArgs &a, cudaStream_t s);   // C0 -> C1
+
+// ---- one state or tile launch (both kernel families take these) --------------------------------
+// One direction of the state recurrence over rows z (dv) and columns y (dqk).
+struct LinStateP {
+    int B, H, T, dqk, dv, G, nseg;
+    int rev;                     // 0: weights l^{e_n-1-s}, segments forwards; 1: scale l^{t-s_n+1}, backwards
+    float scale;                 // used when rev
+    const void *z, *y;           // [B][H][T][dv], [B][H][T][dqk]
+    const float *log_decay;
+    const int32_t *lens;
+    const float *init;           // state the chain starts from, or null (zero)
+    float *sums;                 // U_n [B*H][nseg][dv*dqk]
+    void *states;                // state entering each segment [B*H][nseg][dv*dqk]
+    float *last;                 // state the chain ends in, or null
+};
+// One output: out_t = scale sum_s l^{|t-s|} (x_t.y_s) z_s (s on t's past or future side) + rho_t (state of t's segment) x_t.
+struct LinTileP {
+    int B, H, T, dx, dz, G, nseg;
+    int rev;                     // 0: s <= t, rho = scale l^{t-s_n+1}; 1: s >= t, rho = l^{e_n-1-t}
+    int state_t;                 // states are [dz][dx] (0) or [dx][dz] (1)
+    int has_init;                // the chain's first segment has a state to read
+    float scale;
+    const void *x, *y, *z;
+    const float *log_decay;
+    const int32_t *lens;
+    const void *states;          // [B*H][nseg][..]
+    void *out;                   // [B][H][T][dz], the inputs' type
+};
+
+// ---- device helpers ---------------------------------------------------------------------------------
+// The head's log decay: above 0 reads as 0 (no decay); -inf as the lowest value whose multiples stay finite.
+__device__ __forceinline__ float head_log_decay(const float *ld, int h) {
+    const float x = ld[h];
+    return x > 0.f ? 0.f : (x < -1e30f ? -1e30f : x);
+}
+// l^n for 0 <= n <= 2^24.  The product's rounding error goes into the exponential's argument to first order:
+// without it the relative error would grow with |log_decay n|.
+__device__ __forceinline__ float decay_pow(float ld, int n) {
+    const float x = ld * (float)n, lo = fmaf(ld, (float)n, -x), e = expf(x);
+    return fmaf(e, lo, e);
+}
+__device__ __forceinline__ int seq_len(const int32_t *lens, int b, int T) {
+    return lens ? min(max(lens[b], 0), T) : T;
+}
+
+}  // namespace xlstm
