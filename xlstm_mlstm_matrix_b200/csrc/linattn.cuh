@@ -70,6 +70,13 @@ struct LinTileP {
     void *out;                   // [B][H][T][dz], the inputs' type
 };
 
+// The launches behind both calls; grids stay below 2^31 blocks by the checks of the C ABI.
+cudaError_t linattn_sums_simt(const LinStateP &p, cudaStream_t s);                    // fp32
+cudaError_t linattn_tile_simt(const LinTileP &p, cudaStream_t s);
+cudaError_t linattn_sums_tc(const LinStateP &p, int32_t *status, cudaStream_t s);     // bf16
+cudaError_t linattn_tile_tc(const LinTileP &p, int32_t *status, cudaStream_t s);
+cudaError_t linattn_chain(const LinStateP &p, bool bf16, cudaStream_t s);             // sums -> states in the inputs' type
+
 // ---- device helpers ---------------------------------------------------------------------------------
 // The head's log decay: above 0 reads as 0 (no decay); -inf as the lowest value whose multiples stay finite.
 __device__ __forceinline__ float head_log_decay(const float *ld, int h) {

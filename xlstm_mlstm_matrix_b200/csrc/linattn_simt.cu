@@ -13,16 +13,7 @@ constexpr int kThreads = 256;
 constexpr int kPad = 68;      // row pitch of the transposed 64-wide tiles (4-float aligned, spreads banks)
 constexpr int kK = 32;        // inner-product columns staged at a time
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
@@ -31,8 +22,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
 
 // 64 rows x kK columns of a row-major matrix (nrows x ncols, rows `pitch` apart) into dst[column][row];
 // zeros outside it.
-template <typename T>
-__device__ __forceinline__ void stage_cols(float *dst, const T *src, size_t pitch, int nrows, int col0, int ncols) {
+__device__ __forceinline__ void stage_cols(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
 #pragma unroll
     for (int i = 0; i < 64 * kK / 4 / kThreads; ++i) {
         const int e = threadIdx.x + i * kThreads, r = e & 63, c = (e >> 6) * 4;
@@ -45,8 +35,8 @@ __device__ __forceinline__ void stage_cols(float *dst, const T *src, size_t pitc
     }
 }
 // kK rows x W columns into dst[row][column]; zeros outside.
-template <int W, typename T>
-__device__ __forceinline__ void stage_rows(float *dst, const T *src, size_t pitch, int nrows, int col0, int ncols) {
+template <int W>
+__device__ __forceinline__ void stage_rows(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
 #pragma unroll
     for (int i = 0; i < kK * W / 4 / kThreads; ++i) {
         const int e = threadIdx.x + i * kThreads, r = e / (W / 4), c = (e % (W / 4)) * 4;
@@ -77,7 +67,7 @@ __device__ __forceinline__ void tile_fma(float (&acc)[N][4][4], const float *a, 
 }
 
 // ---- U_n = sum_s w_s z_s y_s^T of one segment, 64 z rows x 64 N y columns per block ------------------
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(kThreads) sums_kernel(LinStateP p, int ztiles, int ytiles) {
     __shared__ __align__(16) float Zs[kK * 64];
     __shared__ __align__(16) float Ys[kK * 64 * N];
@@ -91,8 +81,8 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(LinStateP p, int ztiles,
     const float ld = head_log_decay(p.log_decay, bh % p.H);
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const int z0 = zt * 64, y0 = yt * 64 * N;
-    const T *z = static_cast<const T *>(p.z) + (size_t)bh * p.T * p.dv;
-    const T *y = static_cast<const T *>(p.y) + (size_t)bh * p.T * p.dqk;
+    const float *z = static_cast<const float *>(p.z) + (size_t)bh * p.T * p.dv;
+    const float *y = static_cast<const float *>(p.y) + (size_t)bh * p.T * p.dqk;
     float acc[N][4][4] = {};
     for (int s = s0; s < e; s += kK) {
         const int rows = min(kK, e - s);
@@ -162,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(LinStateP p, int per_he
 }
 
 // ---- output tiles: 64 tokens x 64 N columns per block ---------------------------------------------------
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(kThreads) tile_kernel(LinTileP p, int ttiles, int ztiles) {
     extern __shared__ __align__(16) float sm[];
     float *Xs = sm;                    // [kK][kPad]
@@ -175,15 +165,15 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(LinTileP p, int ttiles, 
     const int tt = id % ttiles, bh = id / ttiles;
     const int len = seq_len(p.lens, bh / p.H, p.T), t0 = tt * 64, z0 = zt * 64 * N;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    T *out = static_cast<T *>(p.out) + (size_t)bh * p.T * p.dz;
+    float *out = static_cast<float *>(p.out) + (size_t)bh * p.T * p.dz;
     float acc[N][4][4] = {};
     if (t0 < len) {
         const float ld = head_log_decay(p.log_decay, bh % p.H);
         const int n = t0 / p.G, s0 = n * p.G, e = min(s0 + p.G, len);
         for (int i = tid; i <= p.G; i += kThreads) pw[i] = decay_pow(ld, i);
-        const T *x = static_cast<const T *>(p.x) + ((size_t)bh * p.T + t0) * p.dx;
-        const T *y = static_cast<const T *>(p.y) + (size_t)bh * p.T * p.dx;
-        const T *z = static_cast<const T *>(p.z) + (size_t)bh * p.T * p.dz;
+        const float *x = static_cast<const float *>(p.x) + ((size_t)bh * p.T + t0) * p.dx;
+        const float *y = static_cast<const float *>(p.y) + (size_t)bh * p.T * p.dx;
+        const float *z = static_cast<const float *>(p.z) + (size_t)bh * p.T * p.dz;
         const int xrows = min(64, len - t0);
         __syncthreads();
         // the entering state's part
@@ -268,115 +258,40 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(LinTileP p, int ttiles, 
     }
 }
 
-constexpr int kSeg = 128;   // tokens of a segment (a multiple of the 64-token tile)
-
 int wide(int d) { return d > 128 ? 4 : d > 64 ? 2 : 1; }
 
-template <typename T>
-cudaError_t sums(const LinStateP &p, cudaStream_t s) {
-    const int N = wide(p.dqk), zt = (p.dv + 63) / 64, yt = (p.dqk + 64 * N - 1) / (64 * N);
-    const long long blocks = (long long)p.B * p.H * p.nseg * zt * yt;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (N == 1) sums_kernel<T, 1><<<(unsigned)blocks, kThreads, 0, s>>>(p, zt, yt);
-    else if (N == 2) sums_kernel<T, 2><<<(unsigned)blocks, kThreads, 0, s>>>(p, zt, yt);
-    else sums_kernel<T, 4><<<(unsigned)blocks, kThreads, 0, s>>>(p, zt, yt);
-    return cudaGetLastError();
-}
-
-template <typename T, int N>
+template <int N>
 cudaError_t tile_n(const LinTileP &p, cudaStream_t s) {
     const int tt = (p.T + 63) / 64, zt = (p.dz + 64 * N - 1) / (64 * N);
-    const long long blocks = (long long)p.B * p.H * tt * zt;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const size_t smem = sizeof(float) * (2 * kK * kPad + 64 * kPad + kK * 64 * N + p.G + 1);
-    cudaError_t e = cudaFuncSetAttribute(tile_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(tile_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    tile_kernel<T, N><<<(unsigned)blocks, kThreads, smem, s>>>(p, tt, zt);
+    tile_kernel<N><<<(unsigned)((size_t)p.B * p.H * tt * zt), kThreads, smem, s>>>(p, tt, zt);
     return cudaGetLastError();
-}
-template <typename T>
-cudaError_t tile(const LinTileP &p, cudaStream_t s) {
-    const int N = wide(p.dz);
-    return N == 1 ? tile_n<T, 1>(p, s) : N == 2 ? tile_n<T, 2>(p, s) : tile_n<T, 4>(p, s);
-}
-
-template <typename S>
-cudaError_t chain(const LinStateP &p, cudaStream_t s) {
-    const int per_head = (int)(((size_t)p.dv * p.dqk / 4 + kThreads - 1) / kThreads);
-    const long long blocks = (long long)p.B * p.H * per_head;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    chain_kernel<S><<<(unsigned)blocks, kThreads, 0, s>>>(p, per_head);
-    return cudaGetLastError();
-}
-
-size_t states_bytes(const LinAttnArgs &a) {
-    return (size_t)a.B * a.H * ((a.T + kSeg - 1) / kSeg) * a.dv * a.dqk * 4;
-}
-
-LinStateP state_params(const LinAttnArgs &a, bool rev) {
-    LinStateP p{};
-    p.B = a.B; p.H = a.H; p.T = a.T; p.dqk = a.dqk; p.dv = a.dv; p.G = kSeg; p.nseg = (a.T + kSeg - 1) / kSeg;
-    p.rev = rev; p.scale = a.scale; p.log_decay = a.log_decay; p.lens = a.lens;
-    p.z = rev ? a.do_ : a.v;
-    p.y = rev ? a.q : a.k;
-    p.init = rev ? a.dC1 : a.C0;
-    p.last = rev ? a.dC0 : a.C1;
-    return p;
-}
-
-LinTileP tile_params(const LinAttnArgs &a, bool rev, const void *x, const void *y, const void *z, int dx, int dz,
-                     bool state_t, const void *states, void *out) {
-    LinTileP p{};
-    p.B = a.B; p.H = a.H; p.T = a.T; p.dx = dx; p.dz = dz; p.G = kSeg; p.nseg = (a.T + kSeg - 1) / kSeg;
-    p.rev = rev; p.state_t = state_t; p.has_init = rev ? a.dC1 != nullptr : a.C0 != nullptr;
-    p.scale = a.scale; p.x = x; p.y = y; p.z = z; p.log_decay = a.log_decay; p.lens = a.lens;
-    p.states = states; p.out = out;
-    return p;
-}
-
-template <typename T>
-cudaError_t states(const LinAttnArgs &a, bool rev, float *ws, cudaStream_t s) {
-    LinStateP p = state_params(a, rev);
-    p.sums = ws;
-    p.states = ws;
-    if (p.nseg == 1 && !p.init && !p.last) return cudaSuccess;   // nothing enters, nothing is handed on
-    if (p.nseg > 1 || p.last) {
-        cudaError_t e = sums<T>(p, s);
-        if (e != cudaSuccess) return e;
-    }
-    return chain<float>(p, s);
-}
-
-template <typename T>
-cudaError_t fwd(const LinAttnArgs &a, cudaStream_t s) {
-    float *ws = static_cast<float *>(a.workspace);
-    cudaError_t e = states<T>(a, false, ws, s);
-    if (e != cudaSuccess) return e;
-    return tile<T>(tile_params(a, false, a.q, a.k, a.v, a.dqk, a.dv, false, ws, a.o), s);
-}
-
-template <typename T>
-cudaError_t bwd(const LinAttnArgs &a, cudaStream_t s) {
-    float *wsC = static_cast<float *>(a.workspace), *wsE = wsC + states_bytes(a) / 4;
-    LinAttnArgs f = a;
-    f.C1 = nullptr;
-    cudaError_t e = states<T>(f, false, wsC, s);
-    if (e == cudaSuccess) e = states<T>(a, true, wsE, s);
-    if (e == cudaSuccess) e = tile<T>(tile_params(a, false, a.do_, a.v, a.k, a.dv, a.dqk, true, wsC, a.dq), s);
-    if (e == cudaSuccess) e = tile<T>(tile_params(a, true, a.v, a.do_, a.q, a.dv, a.dqk, true, wsE, a.dk), s);
-    if (e == cudaSuccess) e = tile<T>(tile_params(a, true, a.k, a.q, a.do_, a.dqk, a.dv, false, wsE, a.dv_), s);
-    return e;
 }
 
 }  // namespace
 
-size_t linattn_workspace_bytes(const LinAttnArgs &a, bool backward) { return (backward ? 2 : 1) * states_bytes(a); }
-
-cudaError_t launch_linattn_fwd(const LinAttnArgs &a, cudaStream_t s) {
-    return a.dtype == XLSTM_BF16 ? fwd<__nv_bfloat16>(a, s) : fwd<float>(a, s);
+cudaError_t linattn_sums_simt(const LinStateP &p, cudaStream_t s) {
+    const int N = wide(p.dqk), zt = (p.dv + 63) / 64, yt = (p.dqk + 64 * N - 1) / (64 * N);
+    const unsigned blocks = (unsigned)((size_t)p.B * p.H * p.nseg * zt * yt);
+    if (N == 1) sums_kernel<1><<<blocks, kThreads, 0, s>>>(p, zt, yt);
+    else if (N == 2) sums_kernel<2><<<blocks, kThreads, 0, s>>>(p, zt, yt);
+    else sums_kernel<4><<<blocks, kThreads, 0, s>>>(p, zt, yt);
+    return cudaGetLastError();
 }
-cudaError_t launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t s) {
-    return a.dtype == XLSTM_BF16 ? bwd<__nv_bfloat16>(a, s) : bwd<float>(a, s);
+
+cudaError_t linattn_tile_simt(const LinTileP &p, cudaStream_t s) {
+    const int N = wide(p.dz);
+    return N == 1 ? tile_n<1>(p, s) : N == 2 ? tile_n<2>(p, s) : tile_n<4>(p, s);
+}
+
+cudaError_t linattn_chain(const LinStateP &p, bool bf16, cudaStream_t s) {
+    const int per_head = (int)(((size_t)p.dv * p.dqk / 4 + kThreads - 1) / kThreads);
+    const unsigned blocks = (unsigned)((size_t)p.B * p.H * per_head);
+    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(p, per_head);
+    else chain_kernel<float><<<blocks, kThreads, 0, s>>>(p, per_head);
+    return cudaGetLastError();
 }
 
 }  // namespace xlstm
