@@ -20,11 +20,12 @@ namespace xlstm {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kV = 8;   // channels of one access per lane
+constexpr int kV = 8, kP = kV / 2;   // channels of one access per lane, and pairs of them
 
 struct GroupNormP {
     int B, T, G, D, heads_major, act, tokens, tokens_per_block;
-    float eps;
+    uint32_t t_mul, t_shift;    // division by T
+    float eps, inv_D;
     const void *x;
     const float *weight, *bias;
     const void *gate, *dy;
@@ -33,36 +34,65 @@ struct GroupNormP {
     float *part_w, *part_b;     // [blocks per group][G * D], null where not asked for
 };
 
+// Eight consecutive values of a tensor in the block's shared memory, as kUnits 16-byte units kThreads apart: each
+// thread copies its own values there asynchronously and reads back only those, so no barrier is needed.
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)     // 0 source bytes: zeros
+                 : "memory");
+}
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&r)[kV]);
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&r)[kV]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w; r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&r)[kV]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Slot {
+    static constexpr int kUnits = sizeof(T) / 2;
+    static __device__ __forceinline__ void copy(uint4 *s, const T *p, bool live) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = __uint_as_float(w[i] << 16);
-        r[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < kUnits; ++i) copy16(s + i * kThreads, p + 4 * i * (kUnits - 1), live);
     }
+    static __device__ __forceinline__ void get(const uint4 *s, float2 (&r)[kP]) {
+        const uint4 a = s[0];
+        if (kUnits == 1) {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                r[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        } else {
+            const uint4 b = s[kThreads * (kUnits - 1)];
+            r[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+            r[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+            r[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+            r[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        }
+    }
+};
+// Shared memory of `tensors_y` tensors of Ty beside x, and how many rows are on their way per warp.
+template <typename Tx, typename Ty, int NV, int TENSORS_Y>
+struct Pipe {
+    static constexpr int X = 0, Y0 = NV * Slot<Tx>::kUnits;     // in units of kThreads
+    static constexpr int UNITS = Y0 + TENSORS_Y * NV * Slot<Ty>::kUnits;
+    static constexpr int STAGE = UNITS * kThreads;
+    static constexpr int STAGES = 65536 / (16 * STAGE) >= 4 ? 4 : 65536 / (16 * STAGE) >= 2 ? 3 : 2;
+    static constexpr int BYTES = STAGES * STAGE * 16;
+};
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void store8(float *p, const float (&r)[kV]) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(r[0], r[1], r[2], r[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(r[4], r[5], r[6], r[7]));
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ void store8(float *p, const float2 (&r)[kP]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(r[0].x, r[0].y, r[1].x, r[1].y));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(r[2].x, r[2].y, r[3].x, r[3].y));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&r)[kV]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float2 (&r)[kP]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(r[2 * i], r[2 * i + 1]);
+    for (int i = 0; i < kP; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(r[i].x, r[i].y);
         w[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Sum over the LPR lanes that share a row.
 template <int LPR>
@@ -72,184 +102,267 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// e^x through the hardware's base-2 exponential: a few units of 2^-23 at these arguments; x -> inf gives 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float act_value(int act, float x) {
-    return act == XLSTM_ACT_NONE ? x : act == XLSTM_ACT_SILU ? x * sigmoid(x) : sigmoid(x);
+// 1 / (1 + e^-x) from the hardware's base-2 exponential and reciprocal, each good to 2^-22; e^-x = inf gives 0.
+__device__ __forceinline__ float sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+__device__ __forceinline__ float2 act_value(int act, float2 x) {
+    if (act == XLSTM_ACT_NONE) return x;
+    const float2 p = make_float2(sigmoid(x.x), sigmoid(x.y));
+    return act == XLSTM_ACT_SILU ? __fmul2_rn(x, p) : p;
 }
 // act(x) and its derivative
-__device__ __forceinline__ void act_both(int act, float x, float &f, float &df) {
+__device__ __forceinline__ void act_both(int act, float2 x, float2 &f, float2 &df) {
     if (act == XLSTM_ACT_NONE) {
-        f = x; df = 1.f;
+        f = x;
+        df = both(1.f);
         return;
     }
-    const float p = sigmoid(x);
+    const float2 p = make_float2(sigmoid(x.x), sigmoid(x.y)), q = __ffma2_rn(p, both(-1.f), both(1.f));   // q = 1 - p
     if (act == XLSTM_ACT_SILU) {
-        f = x * p; df = p * (1.f + x * (1.f - p));
+        f = __fmul2_rn(x, p);
+        df = __fmul2_rn(p, __ffma2_rn(x, q, both(1.f)));
     } else {
-        f = p; df = p * (1.f - p);
+        f = p;
+        df = __fmul2_rn(p, q);
     }
 }
 
-// LPR lanes per row, NV accesses of kV channels per lane.
-template <int LPR, int NV>
-struct Lane {
-    int col[NV];
-    bool in[NV];
-    float w[NV][kV], b[NV][kV];
-    __device__ __forceinline__ Lane(const GroupNormP &p, int g) {
-        const int lcol = threadIdx.x % LPR;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            col[v] = kV * (lcol + v * LPR);
-            in[v] = col[v] < p.D;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int c = g * p.D + col[v] + i;
-                w[v][i] = in[v] && p.weight ? __ldg(p.weight + c) : 1.f;
-                b[v][i] = in[v] && p.bias ? __ldg(p.bias + c) : 0.f;
-            }
-        }
-    }
-};
-
+// n / d for 0 <= n < 2^31: the quotient by a product with ceil-like 2^(32+shift) / d.
+__device__ __forceinline__ int quotient(int n, uint32_t mul, uint32_t shift) {
+    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
+}
 __device__ __forceinline__ size_t x_offset(const GroupNormP &p, int token, int g) {
     if (!p.heads_major) return ((size_t)token * p.G + g) * p.D;
-    const int b = token / p.T, t = token - b * p.T;
+    const int b = quotient(token, p.t_mul, p.t_shift), t = token - b * p.T;
     return (((size_t)b * p.G + g) * p.T + t) * p.D;
 }
 
-// Centres the lane's values and returns the row's rstd.
-template <int LPR, int NV>
-__device__ __forceinline__ float centre(const GroupNormP &p, const Lane<LPR, NV> &ln, float (&x)[NV][kV]) {
-    const float inv = 1.f / (float)p.D;
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) s += x[v][i];   // 0 past D
-    const float mu = row_sum<LPR>(s) * inv;
-    float q = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            x[v][i] = ln.in[v] ? x[v][i] - mu : 0.f;
-            q = fmaf(x[v][i], x[v][i], q);
-        }
-    return 1.f / sqrtf(fmaf(row_sum<LPR>(q), inv, p.eps));
+// weight and bias of the block's group in shared memory (1 and 0 where absent, 0 past D)
+template <int C>
+__device__ __forceinline__ void stage_affine(const GroupNormP &p, int g, float (&w)[C], float (&b)[C]) {
+    for (int c = threadIdx.x; c < C; c += kThreads) {
+        w[c] = c < p.D ? (p.weight ? p.weight[g * p.D + c] : 1.f) : 0.f;
+        b[c] = c < p.D && p.bias ? p.bias[g * p.D + c] : 0.f;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void get8(const float *p, float2 (&r)[kP]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    r[0] = make_float2(a.x, a.y); r[1] = make_float2(a.z, a.w);
+    r[2] = make_float2(b.x, b.y); r[3] = make_float2(b.z, b.w);
 }
 
+// Replaces the lane's values (0 past D) by the normalised ones and returns the row's rstd.
+template <int LPR, int NV>
+__device__ __forceinline__ float normalise(const GroupNormP &p, const bool (&in)[NV], float2 (&x)[NV][kP]) {
+    const float inv = p.inv_D;
+    float2 s = both(0.f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) s = __fadd2_rn(s, x[v][i]);
+    const float2 mu = both(-row_sum<LPR>(s.x + s.y) * inv);
+    float2 q = both(0.f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            x[v][i] = in[v] ? __fadd2_rn(x[v][i], mu) : both(0.f);
+            q = __ffma2_rn(x[v][i], x[v][i], q);
+        }
+    const float rstd = 1.f / sqrtf(fmaf(row_sum<LPR>(q.x + q.y), inv, p.eps));
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) x[v][i] = __fmul2_rn(x[v][i], both(rstd));
+    return rstd;
+}
+
+// LPR lanes per row, NV accesses of eight channels per lane.  A warp's next rows are copied to shared memory while it
+// works on the ones it has: held in registers they cost the occupancy that hides the copies (0.27 ms for the 7B-like
+// layer's 805 MB).
 template <typename Tx, typename Ty, int LPR, int NV>
-__global__ void __launch_bounds__(kThreads) group_norm_kernel(GroupNormP p) {
-    constexpr int RPW = 32 / LPR, U = NV == 1 ? 2 : 1;   // rows per warp and access, rows in flight
+__global__ void __launch_bounds__(kThreads, 3) group_norm_kernel(const GroupNormP p) {
+    using Q = Pipe<Tx, Ty, NV, 1>;
+    constexpr int RPW = 32 / LPR, C = LPR * NV * kV;   // rows per warp, channels covered
+    extern __shared__ uint4 stages[];
+    __shared__ __align__(16) float ws[C], bs[C];
     const int g = blockIdx.x % p.G, base = (blockIdx.x / p.G) * p.tokens_per_block;
     const int end = min(p.tokens, base + p.tokens_per_block);
-    const int warp = threadIdx.x / 32, sub = (threadIdx.x % 32) / LPR;
-    const Lane<LPR, NV> ln(p, g);
+    const int warp = threadIdx.x / 32, sub = (threadIdx.x % 32) / LPR, lcol = threadIdx.x % LPR;
     const Tx *x = static_cast<const Tx *>(p.x);
     const Ty *gate = static_cast<const Ty *>(p.gate);
     Ty *y = static_cast<Ty *>(p.y);
-    for (int r0 = base + warp * RPW * U; r0 < end; r0 += kWarps * RPW * U) {
-        float xv[U][NV][kV], gv[U][NV][kV];
+    bool in[NV];
+    int col[NV];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int row = r0 + u * RPW + sub;
-            const size_t xo = row < end ? x_offset(p, row, g) : 0, yo = ((size_t)row * p.G + g) * p.D;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-#pragma unroll
-                for (int i = 0; i < kV; ++i) xv[u][v][i] = gv[u][v][i] = 0.f;
-                if (row < end && ln.in[v]) {
-                    load8(x + xo + ln.col[v], xv[u][v]);
-                    if (gate) load8(gate + yo + ln.col[v], gv[u][v]);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int row = r0 + u * RPW + sub;
-            const float rstd = centre(p, ln, xv[u]);
-            const size_t yo = ((size_t)row * p.G + g) * p.D;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                float out[kV];
-#pragma unroll
-                for (int i = 0; i < kV; ++i) {
-                    const float z = fmaf(xv[u][v][i] * rstd, ln.w[v][i], ln.b[v][i]);
-                    out[i] = gate ? z * act_value(p.act, gv[u][v][i]) : act_value(p.act, z);
-                }
-                if (row < end && ln.in[v]) store8(y + yo + ln.col[v], out);
-            }
-        }
+    for (int v = 0; v < NV; ++v) {
+        col[v] = kV * (lcol + v * LPR);
+        in[v] = col[v] < p.D;
     }
+    uint4 *own = stages + threadIdx.x;
+    auto fetch = [&](int row, int st) {
+        const bool live = row < end;
+        const size_t xo = live ? x_offset(p, row, g) : 0, yo = live ? ((size_t)row * p.G + g) * p.D : 0;
+        uint4 *s = own + st * Q::STAGE;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool on = live && in[v];
+            Slot<Tx>::copy(s + (Q::X + v * Slot<Tx>::kUnits) * kThreads, x + xo + (on ? col[v] : 0), on);
+            if (gate) Slot<Ty>::copy(s + (Q::Y0 + v * Slot<Ty>::kUnits) * kThreads, gate + yo + (on ? col[v] : 0), on);
+        }
+    };
+    constexpr int step = kWarps * RPW;
+    const int first = base + warp * RPW;
+#pragma unroll
+    for (int k = 0; k < Q::STAGES - 1; ++k) {
+        fetch(first + k * step + sub, k);
+        copies_commit();
+    }
+    stage_affine<C>(p, g, ws, bs);
+    int st = 0;
+    for (int r0 = first; r0 < end; r0 += step) {
+        copies_wait<Q::STAGES - 2>();
+        const uint4 *s = own + st * Q::STAGE;
+        float2 xv[NV][kP];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) Slot<Tx>::get(s + (Q::X + v * Slot<Tx>::kUnits) * kThreads, xv[v]);
+        normalise<LPR, NV>(p, in, xv);
+        const int row = r0 + sub;
+        const size_t yo = ((size_t)row * p.G + g) * p.D;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float2 w[kP], b[kP], out[kP];
+            get8(ws + col[v], w);
+            get8(bs + col[v], b);
+            if (gate) {
+                float2 gv[kP];
+                Slot<Ty>::get(s + (Q::Y0 + v * Slot<Ty>::kUnits) * kThreads, gv);
+#pragma unroll
+                for (int i = 0; i < kP; ++i)
+                    out[i] = __fmul2_rn(__ffma2_rn(xv[v][i], w[i], b[i]), act_value(p.act, gv[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kP; ++i) out[i] = act_value(p.act, __ffma2_rn(xv[v][i], w[i], b[i]));
+            }
+            if (row < end && in[v]) store8(y + yo + col[v], out);
+        }
+        // the stage read one row ago takes the row STAGES - 1 ahead
+        fetch(r0 + (Q::STAGES - 1) * step + sub, (st + Q::STAGES - 1) % Q::STAGES);
+        copies_commit();
+        st = st + 1 == Q::STAGES ? 0 : st + 1;
+    }
+    copies_wait<0>();
 }
 
 template <typename Tx, typename Ty, int LPR, int NV>
-__global__ void __launch_bounds__(kThreads) group_norm_bwd_kernel(GroupNormP p) {
-    constexpr int RPW = 32 / LPR;
-    __shared__ float red[kWarps][LPR * NV * kV];
+__global__ void __launch_bounds__(kThreads, 2) group_norm_bwd_kernel(const GroupNormP p) {
+    using Q = Pipe<Tx, Ty, NV, 2>;
+    constexpr int RPW = 32 / LPR, C = LPR * NV * kV;
+    extern __shared__ uint4 stages[];
+    __shared__ __align__(16) float ws[C], bs[C];
+    __shared__ float red[kWarps][C];
     const int g = blockIdx.x % p.G, chunk = blockIdx.x / p.G, base = chunk * p.tokens_per_block;
     const int end = min(p.tokens, base + p.tokens_per_block);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane / LPR;
-    const Lane<LPR, NV> ln(p, g);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane / LPR, lcol = threadIdx.x % LPR;
     const Tx *x = static_cast<const Tx *>(p.x);
     const Ty *gate = static_cast<const Ty *>(p.gate), *dy = static_cast<const Ty *>(p.dy);
     Tx *dx = static_cast<Tx *>(p.y);
     Ty *dgate = static_cast<Ty *>(p.dgate);
-    const float inv = 1.f / (float)p.D;
-    float sw[NV][kV] = {}, sb[NV][kV] = {};
-    for (int r0 = base + warp * RPW; r0 < end; r0 += kWarps * RPW) {
+    bool in[NV];
+    int col[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        col[v] = kV * (lcol + v * LPR);
+        in[v] = col[v] < p.D;
+    }
+    uint4 *own = stages + threadIdx.x;
+    auto fetch = [&](int row, int st) {
+        const bool live = row < end;
+        const size_t xo = live ? x_offset(p, row, g) : 0, yo = live ? ((size_t)row * p.G + g) * p.D : 0;
+        uint4 *s = own + st * Q::STAGE;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool on = live && in[v];
+            const int c = on ? col[v] : 0;
+            Slot<Tx>::copy(s + (Q::X + v * Slot<Tx>::kUnits) * kThreads, x + xo + c, on);
+            Slot<Ty>::copy(s + (Q::Y0 + v * Slot<Ty>::kUnits) * kThreads, dy + yo + c, on);
+            if (gate) Slot<Ty>::copy(s + (Q::Y0 + (NV + v) * Slot<Ty>::kUnits) * kThreads, gate + yo + c, on);
+        }
+    };
+    float2 sw[NV][kP], sb[NV][kP];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) sw[v][i] = sb[v][i] = both(0.f);
+    constexpr int step = kWarps * RPW;
+    const int first = base + warp * RPW;
+#pragma unroll
+    for (int k = 0; k < Q::STAGES - 1; ++k) {
+        fetch(first + k * step + sub, k);
+        copies_commit();
+    }
+    stage_affine<C>(p, g, ws, bs);
+    int st = 0;
+    for (int r0 = first; r0 < end; r0 += step) {
         const int row = r0 + sub;
         const bool live = row < end;
-        const size_t xo = live ? x_offset(p, row, g) : 0, yo = ((size_t)row * p.G + g) * p.D;
-        float xv[NV][kV], gv[NV][kV], dv[NV][kV];
+        const size_t yo = ((size_t)row * p.G + g) * p.D;
+        copies_wait<Q::STAGES - 2>();
+        const uint4 *s = own + st * Q::STAGE;
+        float2 xv[NV][kP], dv[NV][kP];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) Slot<Tx>::get(s + (Q::X + v * Slot<Tx>::kUnits) * kThreads, xv[v]);
+        const float rstd = normalise<LPR, NV>(p, in, xv);
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            float2 w[kP], b[kP];
+            float2 gv[kP];
+            get8(ws + col[v], w);
+            get8(bs + col[v], b);
+            Slot<Ty>::get(s + (Q::Y0 + v * Slot<Ty>::kUnits) * kThreads, dv[v]);
+            if (gate) Slot<Ty>::get(s + (Q::Y0 + (NV + v) * Slot<Ty>::kUnits) * kThreads, gv);
 #pragma unroll
-            for (int i = 0; i < kV; ++i) xv[v][i] = gv[v][i] = dv[v][i] = 0.f;
-            if (live && ln.in[v]) {
-                load8(x + xo + ln.col[v], xv[v]);
-                load8(dy + yo + ln.col[v], dv[v]);
-                if (gate) load8(gate + yo + ln.col[v], gv[v]);
-            }
-        }
-        const float rstd = centre(p, ln, xv);
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float xh = xv[v][i] * rstd, z = fmaf(xh, ln.w[v][i], ln.b[v][i]);
-                float f, df, dz;
+            for (int i = 0; i < kP; ++i) {
+                const float2 z = __ffma2_rn(xv[v][i], w[i], b[i]);
+                float2 f, df, dz;
                 if (gate) {
-                    act_both(p.act, gv[v][i], f, df);
-                    dz = dv[v][i] * f;
-                    gv[v][i] = dv[v][i] * z * df;
+                    act_both(p.act, gv[i], f, df);
+                    dz = __fmul2_rn(dv[v][i], f);
+                    gv[i] = __fmul2_rn(__fmul2_rn(dv[v][i], z), df);
                 } else {
                     act_both(p.act, z, f, df);
-                    dz = dv[v][i] * df;
+                    dz = __fmul2_rn(dv[v][i], df);
                 }
-                sw[v][i] = fmaf(dz, xh, sw[v][i]);
-                sb[v][i] += dz;
-                dz *= ln.w[v][i];
-                s1 += dz;
-                s2 = fmaf(dz, xh, s2);
+                sw[v][i] = __ffma2_rn(dz, xv[v][i], sw[v][i]);
+                sb[v][i] = __fadd2_rn(sb[v][i], dz);
+                dz = __fmul2_rn(dz, w[i]);
+                s1 = __fadd2_rn(s1, dz);
+                s2 = __ffma2_rn(dz, xv[v][i], s2);
                 dv[v][i] = dz;
-                xv[v][i] = xh;
             }
-            if (gate && live && ln.in[v]) store8(dgate + yo + ln.col[v], gv[v]);
+            if (gate && live && in[v]) store8(dgate + yo + col[v], gv);
         }
-        s1 = row_sum<LPR>(s1) * inv;
-        s2 = row_sum<LPR>(s2) * inv;
+        const float m1 = row_sum<LPR>(s1.x + s1.y) * p.inv_D, m2 = row_sum<LPR>(s2.x + s2.y) * p.inv_D;
+        const size_t xo = live ? x_offset(p, row, g) : 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float out[kV];
+            float2 out[kP];
 #pragma unroll
-            for (int i = 0; i < kV; ++i) out[i] = rstd * (dv[v][i] - s1 - xv[v][i] * s2);
-            if (live && ln.in[v]) store8(dx + xo + ln.col[v], out);
+            for (int i = 0; i < kP; ++i)
+                out[i] = __fmul2_rn(both(rstd), __ffma2_rn(xv[v][i], both(-m2), __fadd2_rn(dv[v][i], both(-m1))));
+            if (live && in[v]) store8(dx + xo + col[v], out);
         }
+        fetch(r0 + (Q::STAGES - 1) * step + sub, (st + Q::STAGES - 1) % Q::STAGES);
+        copies_commit();
+        st = st + 1 == Q::STAGES ? 0 : st + 1;
     }
+    copies_wait<0>();
     // this block's sums over its tokens: lanes of the same columns, then warps in order
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
@@ -260,10 +373,11 @@ __global__ void __launch_bounds__(kThreads) group_norm_bwd_kernel(GroupNormP p) 
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                float s = pass ? sb[v][i] : sw[v][i];
+                const float2 t = pass ? sb[v][i / 2] : sw[v][i / 2];
+                float s = i % 2 ? t.y : t.x;
 #pragma unroll
                 for (int o = LPR; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (sub == 0) red[warp][(v * LPR + lane) * kV + i] = s;
+                if (sub == 0) red[warp][col[v] + i] = s;
             }
         __syncthreads();
         for (int c = threadIdx.x; c < p.D; c += kThreads) {
@@ -314,30 +428,34 @@ int bwd_chunks(const xlstm_group_norm_desc_t *d) {
     return (tokens + tpb - 1) / tpb;
 }
 
+template <typename Tx, typename Ty, int LPR, int NV, bool kBwd>
+cudaError_t launch(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
+    constexpr int smem = Pipe<Tx, Ty, NV, kBwd ? 2 : 1>::BYTES;
+    void (*const kernel)(GroupNormP) = kBwd ? group_norm_bwd_kernel<Tx, Ty, LPR, NV> : group_norm_kernel<Tx, Ty, LPR, NV>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
 template <typename Tx, typename Ty, bool kBwd>
-void launch(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
-#define GROUP_NORM(LPR, NV)                                                             \
-    if (kBwd) group_norm_bwd_kernel<Tx, Ty, LPR, NV><<<blocks, kThreads, 0, s>>>(p);    \
-    else group_norm_kernel<Tx, Ty, LPR, NV><<<blocks, kThreads, 0, s>>>(p);
-    if (p.D > 256) { GROUP_NORM(32, 2) return; }
+cudaError_t launch_types(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
+    if (p.D > 256) return launch<Tx, Ty, 32, 2, kBwd>(p, blocks, s);
     switch (lanes_per_row(p.D)) {
-        case 2: GROUP_NORM(2, 1) break;
-        case 4: GROUP_NORM(4, 1) break;
-        case 8: GROUP_NORM(8, 1) break;
-        case 16: GROUP_NORM(16, 1) break;
-        default: GROUP_NORM(32, 1) break;
+        case 2: return launch<Tx, Ty, 2, 1, kBwd>(p, blocks, s);
+        case 4: return launch<Tx, Ty, 4, 1, kBwd>(p, blocks, s);
+        case 8: return launch<Tx, Ty, 8, 1, kBwd>(p, blocks, s);
+        case 16: return launch<Tx, Ty, 16, 1, kBwd>(p, blocks, s);
+        default: return launch<Tx, Ty, 32, 1, kBwd>(p, blocks, s);
     }
-#undef GROUP_NORM
 }
 template <bool kBwd>
 cudaError_t launch_any(const xlstm_group_norm_desc_t *d, const GroupNormP &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)((p.tokens + p.tokens_per_block - 1) / p.tokens_per_block) * p.G;
     const bool xb = d->x_dtype == XLSTM_BF16, yb = d->y_dtype == XLSTM_BF16;
-    if (xb && yb) launch<__nv_bfloat16, __nv_bfloat16, kBwd>(p, blocks, s);
-    else if (xb) launch<__nv_bfloat16, float, kBwd>(p, blocks, s);
-    else if (yb) launch<float, __nv_bfloat16, kBwd>(p, blocks, s);
-    else launch<float, float, kBwd>(p, blocks, s);
-    return cudaGetLastError();
+    if (xb && yb) return launch_types<__nv_bfloat16, __nv_bfloat16, kBwd>(p, blocks, s);
+    if (xb) return launch_types<__nv_bfloat16, float, kBwd>(p, blocks, s);
+    if (yb) return launch_types<float, __nv_bfloat16, kBwd>(p, blocks, s);
+    return launch_types<float, float, kBwd>(p, blocks, s);
 }
 
 bool desc_ok(const xlstm_group_norm_desc_t *d) {
@@ -357,6 +475,9 @@ GroupNormP pack(const xlstm_group_norm_desc_t *d, long long blocks) {
     p.B = d->B; p.T = d->T; p.G = d->G; p.D = d->D; p.heads_major = d->x_layout == XLSTM_HEADS_MAJOR;
     p.act = d->act; p.eps = d->eps; p.tokens = d->B * d->T;
     p.tokens_per_block = tokens_per_block(p.tokens, d->G, d->D, blocks);
+    p.inv_D = 1.f / (float)d->D;
+    while ((1ull << p.t_shift) < (unsigned)d->T) ++p.t_shift;
+    p.t_mul = (uint32_t)(((1ull << 32) * ((1ull << p.t_shift) - (unsigned)d->T)) / (unsigned)d->T + 1);
     return p;
 }
 
