@@ -9,6 +9,7 @@ A missing library raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -458,43 +459,67 @@ def bwd(q, k, v, i_pre, f_pre, dh, state=None, dstate=None, qk_scale=None, strea
 
 
 # ---- xlstm_layer.h: torch conveniences (checks, allocation, marshalling) ------------
-def _want(x, name, shape, dtypes, device):
-    """x is a contiguous tensor of this shape, on this device, of one of these dtypes."""
-    if x.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {x.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(x.shape) != tuple(shape):
+# These calls also serve single tokens, where the host's time is the call's time: shapes are compared as they
+# are, addresses go to ctypes as plain integers, and a shape's descriptor and workspace size are formed once.
+def _want(x, name, shape, dtype, index):
+    """x is a contiguous tensor of this shape and type on CUDA device `index`."""
+    if x.dtype != dtype:
+        raise TypeError(f"{name}: dtype {x.dtype}, expected {dtype}")
+    if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, expected CUDA device {index}")
     if not x.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
 
 
-def _call_on(device, stream):
-    """The device's context and the stream to launch on (the device's current one by default)."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"CUDA tensors expected, got {device}")
-    return torch.cuda.device(device), stream if stream is not None else torch.cuda.current_stream(device)
+def _raw(x):
+    return None if x is None else x.data_ptr()
 
 
-def _linattn_inputs(q, k, v, log_decay, state, lens, token_axis):
+def _run(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current, on its current stream by default."""
     import torch
-    _dtype_code(q)
-    dev, f32 = q.device, (torch.float32,)
-    if q.dim() != 3 + token_axis:
-        raise ValueError(f"q: {q.dim()} axes, expected {3 + token_axis}")
-    B, H, dqk, dv = q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]
-    T = q.shape[2] if token_axis else 1
-    _want(q, "q", q.shape, (q.dtype,), dev)
-    _want(k, "k", q.shape, (q.dtype,), dev)
-    _want(v, "v", (*q.shape[:-1], dv), (q.dtype,), dev)
-    _want(log_decay, "log_decay", (H,), f32, dev)
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
+    stream = torch.cuda.current_stream(index).cuda_stream if stream is None else \
+        stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
+    if st != XLSTM_OK:
+        raise XlstmError(st, fn.__name__)
+
+
+@functools.lru_cache(maxsize=256)
+def _linattn_plan(B, H, T, dqk, dv, dtype, scale):
+    """The descriptor of a shape and its forward and backward workspace sizes."""
+    desc = make_linattn_desc(B, H, T, dqk, dv, dtype, scale)
+    return desc, max(256, xlstm_linattn_workspace_size(desc)), max(256, xlstm_linattn_bwd_workspace_size(desc))
+
+
+def _linattn_inputs(q, k, v, log_decay, state, lens, scale, token_axis):
+    import torch
+    dt, f32 = q.dtype, torch.float32
+    code = _dtype_code(q)
+    if q.dim() != 3 + token_axis or v.dim() != 3 + token_axis:
+        raise ValueError(f"q: {q.dim()} axes, v: {v.dim()} axes, expected {3 + token_axis}")
+    shape, dv = q.shape, v.shape[-1]
+    B, H, dqk = shape[0], shape[1], shape[-1]
+    index = q.get_device()
+    _want(q, "q", shape, dt, index)
+    _want(k, "k", shape, dt, index)
+    _want(v, "v", (*shape[:-1], dv), dt, index)
+    _want(log_decay, "log_decay", (H,), f32, index)
     if state is not None:
-        _want(state, "state", (B, H, dv, dqk), f32, dev)
+        _want(state, "state", (B, H, dv, dqk), f32, index)
     if lens is not None:
-        _want(lens, "lens", (B,), (torch.int32,), dev)
-    return B, H, T, dqk, dv
+        _want(lens, "lens", (B,), torch.int32, index)
+    plan = _linattn_plan(B, H, shape[2] if token_axis else 1, dqk, dv, code,
+                         dqk ** -0.5 if scale is None else float(scale))
+    return index, plan, (B, H, dv, dqk)
 
 
 def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=None, workspace=None, out=None):
@@ -506,22 +531,18 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
     defaults to dqk ** -0.5.  Returns (o, C): o [B,H,T,dv] in q's type and the final state.
     out: (o, C) to write into; C may be None (not formed)."""
     import torch
-    B, H, T, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, lens, 1)
-    dev = q.device
-    desc = make_linattn_desc(B, H, T, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
-    ctx, stream = _call_on(dev, stream)
+    index, (desc, size, _), state_shape = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 1)
     if out is None:
-        o, C = torch.empty_like(v), torch.empty(B, H, dv, dqk, device=dev, dtype=torch.float32)
+        o, C = torch.empty_like(v), torch.empty(state_shape, device=v.device, dtype=torch.float32)
     else:
         o, C = out
-        _want(o, "out[0]", v.shape, (v.dtype,), dev)
+        _want(o, "out[0]", v.shape, v.dtype, index)
         if C is not None:
-            _want(C, "out[1]", (B, H, dv, dqk), (torch.float32,), dev)
-    with ctx:
-        if workspace is None:
-            workspace = torch.empty(max(256, xlstm_linattn_workspace_size(desc)), device=dev, dtype=torch.uint8)
-        check(xlstm_linattn_fwd(desc, q, k, v, log_decay, lens, state, o, C, workspace, workspace.numel(), stream),
-              "xlstm_linattn_fwd")
+            _want(C, "out[1]", state_shape, torch.float32, index)
+    if workspace is None:
+        workspace = torch.empty(size, device=v.device, dtype=torch.uint8)
+    _run(load().xlstm_linattn_fwd, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+         _raw(lens), _raw(state), o.data_ptr(), _raw(C), workspace.data_ptr(), workspace.numel())
     return o, C
 
 
@@ -529,17 +550,15 @@ def linattn_step(q, k, v, log_decay, state, scale=None, stream=None, out=None, i
     """One token per sequence through xlstm_linattn_step.  q, k [B,H,dqk], v [B,H,dv], state [B,H,dv,dqk].
     Returns (o, C'); inplace=True updates state itself.  out: (o, C') to write into."""
     import torch
-    B, H, _, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, None, 0)
-    desc = make_linattn_desc(B, H, 1, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
-    ctx, stream = _call_on(q.device, stream)
+    index, (desc, _, _), state_shape = _linattn_inputs(q, k, v, log_decay, state, None, scale, 0)
     if out is None:
         o, C = torch.empty_like(v), state if inplace else torch.empty_like(state)
     else:
         o, C = out[0], state if inplace else out[1]
-        _want(o, "out[0]", v.shape, (v.dtype,), q.device)
-        _want(C, "out[1]", state.shape, (torch.float32,), q.device)
-    with ctx:
-        check(xlstm_linattn_step(desc, q, k, v, log_decay, state, o, C, stream), "xlstm_linattn_step")
+        _want(o, "out[0]", v.shape, v.dtype, index)
+        _want(C, "out[1]", state_shape, torch.float32, index)
+    _run(load().xlstm_linattn_step, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+         state.data_ptr(), o.data_ptr(), C.data_ptr())
     return o, C
 
 
@@ -547,46 +566,52 @@ def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lens=None, scal
     """Gradients of linattn_fwd through xlstm_linattn_bwd: do is the gradient of o (q's type), dstate that of the
     final state (fp32) or None.  Returns dict(dq, dk, dv, dC0): the inputs' types, dC0 fp32."""
     import torch
-    B, H, T, dqk, dv = _linattn_inputs(q, k, v, log_decay, state, lens, 1)
-    dev = q.device
-    _want(do, "do", v.shape, (v.dtype,), dev)
+    index, (desc, _, size), state_shape = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 1)
+    _want(do, "do", v.shape, v.dtype, index)
     if dstate is not None:
-        _want(dstate, "dstate", (B, H, dv, dqk), (torch.float32,), dev)
-    desc = make_linattn_desc(B, H, T, dqk, dv, _dtype_code(q), dqk ** -0.5 if scale is None else float(scale))
-    ctx, stream = _call_on(dev, stream)
-    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-             dC0=torch.empty(B, H, dv, dqk, device=dev, dtype=torch.float32))
-    with ctx:
-        if workspace is None:
-            workspace = torch.empty(max(256, xlstm_linattn_bwd_workspace_size(desc)), device=dev, dtype=torch.uint8)
-        check(xlstm_linattn_bwd(desc, q, k, v, log_decay, lens, state, do, dstate, g["dq"], g["dk"], g["dv"], g["dC0"],
-                                workspace, workspace.numel(), stream), "xlstm_linattn_bwd")
-    return g
+        _want(dstate, "dstate", state_shape, torch.float32, index)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dC0 = torch.empty(state_shape, device=v.device, dtype=torch.float32)
+    if workspace is None:
+        workspace = torch.empty(size, device=v.device, dtype=torch.uint8)
+    _run(load().xlstm_linattn_bwd, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+         _raw(lens), _raw(state), do.data_ptr(), _raw(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+         dC0.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return dict(dq=dq, dk=dk, dv=dv, dC0=dC0)
 
 
 _LAYOUTS = {"heads": XLSTM_HEADS_MAJOR, "tokens": XLSTM_CHANNELS_LAST}
 _ACTS = {"none": XLSTM_ACT_NONE, "silu": XLSTM_ACT_SILU, "sigmoid": XLSTM_ACT_SIGMOID}
 
 
+@functools.lru_cache(maxsize=256)
+def _group_norm_plan(B, T, G, D, x_dtype, y_dtype, layout, act, eps):
+    """The descriptor of a shape and its backward workspace size."""
+    desc = make_group_norm_desc(B, T, G, D, x_dtype, y_dtype, layout, act, eps)
+    return desc, max(256, xlstm_group_norm_bwd_workspace_size(desc))
+
+
 def _group_norm_inputs(x, weight, bias, gate, act, layout, eps, y_dtype):
     import torch
     if layout not in _LAYOUTS or act not in _ACTS:
         raise ValueError(f"layout {layout!r} (of {sorted(_LAYOUTS)}), act {act!r} (of {sorted(_ACTS)})")
-    both = (torch.float32, torch.bfloat16)
+    code = {torch.float32: XLSTM_F32, torch.bfloat16: XLSTM_BF16}
+    if x.dtype not in code or y_dtype not in code:
+        raise TypeError(f"x and y must be bf16 or fp32, got {x.dtype} and {y_dtype}")
     if x.dim() != 4:
         raise ValueError(f"x: {x.dim()} axes, expected 4")
     B, G, T, D = x.shape if layout == "heads" else (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
-    _want(x, "x", x.shape, both, x.device)
-    for p, name in ((weight, "weight"), (bias, "bias")):
-        if p is not None:
-            _want(p, name, (G * D,), (torch.float32,), x.device)
-    if y_dtype not in both:
-        raise TypeError(f"y must be bf16 or fp32, got {y_dtype}")
+    index = x.get_device()
+    _want(x, "x", x.shape, x.dtype, index)
+    if weight is not None:
+        _want(weight, "weight", (G * D,), torch.float32, index)
+    if bias is not None:
+        _want(bias, "bias", (G * D,), torch.float32, index)
+    shape = (B, T, G * D)
     if gate is not None:
-        _want(gate, "gate", (B, T, G * D), (y_dtype,), x.device)
-    code = {torch.float32: XLSTM_F32, torch.bfloat16: XLSTM_BF16}
-    desc = make_group_norm_desc(B, T, G, D, code[x.dtype], code[y_dtype], _LAYOUTS[layout], _ACTS[act], eps)
-    return desc, (B, T, G * D)
+        _want(gate, "gate", shape, y_dtype, index)
+    plan = _group_norm_plan(B, T, G, D, code[x.dtype], code[y_dtype], _LAYOUTS[layout], _ACTS[act], eps)
+    return index, plan, shape
 
 
 def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads", eps=1e-5, out_dtype=None, stream=None,
@@ -600,14 +625,12 @@ def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads",
     x's, by default)."""
     import torch
     dt = out.dtype if out is not None else out_dtype if out_dtype is not None else gate.dtype if gate is not None else x.dtype
-    desc, shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
-    ctx, stream = _call_on(x.device, stream)
+    index, (desc, _), shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
     if out is None:
         out = torch.empty(shape, device=x.device, dtype=dt)
     else:
-        _want(out, "out", shape, (dt,), x.device)
-    with ctx:
-        check(xlstm_group_norm(desc, x, weight, bias, gate, out, stream), "xlstm_group_norm")
+        _want(out, "out", shape, dt, index)
+    _run(load().xlstm_group_norm, index, stream, desc, x.data_ptr(), _raw(weight), _raw(bias), _raw(gate), out.data_ptr())
     return out
 
 
@@ -616,17 +639,12 @@ def group_norm_bwd(dy, x, weight=None, bias=None, gate=None, act="silu", layout=
     """Gradients of group_norm through xlstm_group_norm_bwd: dict(dx, dgate, dweight, dbias); None in the place of
     what was not given."""
     import torch
-    desc, shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
-    _want(dy, "dy", shape, (dy.dtype,), x.device)
-    ctx, stream = _call_on(x.device, stream)
-    g = dict(dx=torch.empty_like(x), dgate=None if gate is None else torch.empty_like(gate),
-             dweight=None if weight is None else torch.empty_like(weight),
-             dbias=None if bias is None else torch.empty_like(bias))
-    with ctx:
-        if workspace is None and (weight is not None or bias is not None):
-            workspace = torch.empty(max(256, xlstm_group_norm_bwd_workspace_size(desc)), device=x.device,
-                                    dtype=torch.uint8)
-        check(xlstm_group_norm_bwd(desc, x, weight, bias, gate, dy, g["dx"], g["dgate"], g["dweight"], g["dbias"],
-                                   workspace, 0 if workspace is None else workspace.numel(), stream),
-              "xlstm_group_norm_bwd")
-    return g
+    index, (desc, size), shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
+    _want(dy, "dy", shape, dy.dtype, index)
+    dx, dgate, dw, db = torch.empty_like(x), *(None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
+    if workspace is None and (weight is not None or bias is not None):
+        workspace = torch.empty(size, device=x.device, dtype=torch.uint8)
+    _run(load().xlstm_group_norm_bwd, index, stream, desc, x.data_ptr(), _raw(weight), _raw(bias), _raw(gate),
+         dy.data_ptr(), dx.data_ptr(), _raw(dgate), _raw(dw), _raw(db), _raw(workspace),
+         0 if workspace is None else workspace.numel())
+    return dict(dx=dx, dgate=dgate, dweight=dw, dbias=db)

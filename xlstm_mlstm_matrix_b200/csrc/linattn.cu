@@ -6,7 +6,7 @@ namespace {
 
 // Tokens of a segment.
 int segment(const LinAttnArgs &a) {
-    if (a.dtype != XLSTM_BF16) return 128;
+    if (a.dtype != XLSTM_BF16) return kSimtSegment;
     return (size_t)a.dqk * a.dv > 128 * 128 ? 256 : 512;
 }
 
@@ -24,9 +24,7 @@ Plan plan(const LinAttnArgs &a) {
     return p;
 }
 
-// The entering states of all segments (and the chain's end) in one direction; returns where they are.
-cudaError_t states(const LinAttnArgs &a, const Plan &pl, bool rev, char *ws, const void *&where, cudaStream_t s) {
-    const bool bf16 = a.dtype == XLSTM_BF16;
+LinStateP state_job(const LinAttnArgs &a, const Plan &pl, bool rev, char *ws) {
     LinStateP p{};
     p.B = a.B; p.H = a.H; p.T = a.T; p.dqk = a.dqk; p.dv = a.dv; p.G = pl.G; p.nseg = pl.nseg;
     p.rev = rev; p.scale = a.scale; p.log_decay = a.log_decay; p.lens = a.lens;
@@ -35,25 +33,42 @@ cudaError_t states(const LinAttnArgs &a, const Plan &pl, bool rev, char *ws, con
     p.init = rev ? a.dC1 : a.C0;
     p.last = rev ? a.dC0 : a.C1;
     p.sums = reinterpret_cast<float *>(ws);
-    p.states = bf16 ? ws + pl.sums : ws;
-    where = p.states;
-    if (p.nseg == 1 && !p.init && !p.last) return cudaSuccess;   // nothing enters, nothing is handed on
-    if (p.nseg > 1 || p.last) {
-        const cudaError_t e = bf16 ? linattn_sums_tc(p, a.status, s) : linattn_sums_simt(p, s);
-        if (e != cudaSuccess) return e;
+    p.states = a.dtype == XLSTM_BF16 ? ws + pl.sums : ws;
+    return p;
+}
+
+// The entering states of all segments, and the chains' ends.
+cudaError_t run_states(const LinAttnArgs &a, const LinStateP *p, int n, cudaStream_t s) {
+    const bool bf16 = a.dtype == XLSTM_BF16;
+    LinStates sums{}, chains{};
+    for (int i = 0; i < n; ++i) {
+        if (p[i].nseg == 1 && !p[i].init && !p[i].last) continue;     // nothing enters, nothing is handed on
+        if (p[i].nseg > 1 || p[i].last) sums.p[sums.count++] = p[i];
+        chains.p[chains.count++] = p[i];
     }
-    return linattn_chain(p, bf16, s);
+    cudaError_t e = cudaSuccess;
+    if (bf16)
+        for (int i = 0; e == cudaSuccess && i < sums.count; ++i) e = linattn_sums_tc(sums.p[i], a.status, s);
+    else if (sums.count)
+        e = linattn_sums_simt(sums, s);
+    return e == cudaSuccess && chains.count ? linattn_chain(chains, bf16, s) : e;
 }
 
 // out_t = scale sum l^{|t-s|} (x_t.y_s) z_s + rho_t (entering state) x_t
-cudaError_t tile(const LinAttnArgs &a, const Plan &pl, bool rev, const void *x, const void *y, const void *z, int dx,
-                 int dz, bool state_t, const void *states, void *out, cudaStream_t s) {
+LinTileP tile_job(const LinAttnArgs &a, const LinStateP &st, const void *x, const void *y, const void *z, int dx, int dz,
+                  bool state_t, void *out) {
     LinTileP p{};
-    p.B = a.B; p.H = a.H; p.T = a.T; p.dx = dx; p.dz = dz; p.G = pl.G; p.nseg = pl.nseg;
-    p.rev = rev; p.state_t = state_t; p.has_init = rev ? a.dC1 != nullptr : a.C0 != nullptr;
+    p.B = a.B; p.H = a.H; p.T = a.T; p.dx = dx; p.dz = dz; p.G = st.G; p.nseg = st.nseg;
+    p.rev = st.rev; p.state_t = state_t; p.has_init = st.init != nullptr;
     p.scale = a.scale; p.x = x; p.y = y; p.z = z; p.log_decay = a.log_decay; p.lens = a.lens;
-    p.states = states; p.out = out;
-    return a.dtype == XLSTM_BF16 ? linattn_tile_tc(p, a.status, s) : linattn_tile_simt(p, s);
+    p.states = st.states; p.out = out;
+    return p;
+}
+cudaError_t run_tiles(const LinAttnArgs &a, const LinTiles &jobs, cudaStream_t s) {
+    if (a.dtype != XLSTM_BF16) return linattn_tile_simt(jobs, a.status, s);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; e == cudaSuccess && i < jobs.count; ++i) e = linattn_tile_tc(jobs.p[i], a.status, s);
+    return e;
 }
 
 }  // namespace
@@ -64,22 +79,25 @@ size_t linattn_workspace_bytes(const LinAttnArgs &a, bool backward) {
 }
 
 cudaError_t launch_linattn_fwd(const LinAttnArgs &a, cudaStream_t s) {
-    const Plan pl = plan(a);
-    const void *C;
-    const cudaError_t e = states(a, pl, false, static_cast<char *>(a.workspace), C, s);
-    return e != cudaSuccess ? e : tile(a, pl, false, a.q, a.k, a.v, a.dqk, a.dv, false, C, a.o, s);
+    const LinStateP C = state_job(a, plan(a), false, static_cast<char *>(a.workspace));
+    const cudaError_t e = run_states(a, &C, 1, s);
+    if (e != cudaSuccess) return e;
+    LinTiles t{};
+    t.p[t.count++] = tile_job(a, C, a.q, a.k, a.v, a.dqk, a.dv, false, a.o);
+    return run_tiles(a, t, s);
 }
 
 cudaError_t launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t s) {
     const Plan pl = plan(a);
     char *ws = static_cast<char *>(a.workspace);
-    const void *C, *E;
-    cudaError_t e = states(a, pl, false, ws, C, s);
-    if (e == cudaSuccess) e = states(a, pl, true, ws + pl.sums + pl.states, E, s);
-    if (e == cudaSuccess) e = tile(a, pl, false, a.do_, a.v, a.k, a.dv, a.dqk, true, C, a.dq, s);
-    if (e == cudaSuccess) e = tile(a, pl, true, a.v, a.do_, a.q, a.dv, a.dqk, true, E, a.dk, s);
-    if (e == cudaSuccess) e = tile(a, pl, true, a.k, a.q, a.do_, a.dqk, a.dv, false, E, a.dv_, s);
-    return e;
+    const LinStateP p[2] = {state_job(a, pl, false, ws), state_job(a, pl, true, ws + pl.sums + pl.states)};
+    const cudaError_t e = run_states(a, p, 2, s);
+    if (e != cudaSuccess) return e;
+    LinTiles t{};
+    t.p[t.count++] = tile_job(a, p[0], a.do_, a.v, a.k, a.dv, a.dqk, true, a.dq);
+    t.p[t.count++] = tile_job(a, p[1], a.v, a.do_, a.q, a.dv, a.dqk, true, a.dk);
+    t.p[t.count++] = tile_job(a, p[1], a.k, a.q, a.do_, a.dqk, a.dv, false, a.dv_);
+    return run_tiles(a, t, s);
 }
 
 }  // namespace xlstm

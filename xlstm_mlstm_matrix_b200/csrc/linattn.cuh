@@ -70,12 +70,33 @@ struct LinTileP {
     void *out;                   // [B][H][T][dz], the inputs' type
 };
 
+// The directions (forwards; forwards and backwards) or outputs (o; dq, dk and dv) of one call: they do not depend on
+// one another, so a launch takes them all, job after job over its blocks.
+template <typename P, int MOST>
+struct LinJobs {
+    P p[MOST];
+    int count;
+    unsigned end[MOST];      // blocks of the jobs up to and including this one
+};
+using LinStates = LinJobs<LinStateP, 2>;
+using LinTiles = LinJobs<LinTileP, 3>;
+// The job of a block, and the block's number within it.
+template <typename P, int MOST>
+__device__ __forceinline__ int job_of_block(const LinJobs<P, MOST> &jobs, unsigned &block) {
+    int j = 0;
+    block = blockIdx.x;
+    while (j + 1 < jobs.count && block >= jobs.end[j]) ++j;
+    if (j) block -= jobs.end[j - 1];
+    return j;
+}
+
 // The launches behind both calls; grids stay below 2^31 blocks by the checks of the C ABI.
-cudaError_t linattn_sums_simt(const LinStateP &p, cudaStream_t s);                    // fp32
-cudaError_t linattn_tile_simt(const LinTileP &p, cudaStream_t s);
+constexpr int kSimtSegment = 64;                                              // the fp32 kernels' G
+cudaError_t linattn_sums_simt(LinStates jobs, cudaStream_t s);                     // fp32
+cudaError_t linattn_tile_simt(LinTiles jobs, int32_t *status, cudaStream_t s);     // clears status
 cudaError_t linattn_sums_tc(const LinStateP &p, int32_t *status, cudaStream_t s);     // bf16
 cudaError_t linattn_tile_tc(const LinTileP &p, int32_t *status, cudaStream_t s);
-cudaError_t linattn_chain(const LinStateP &p, bool bf16, cudaStream_t s);             // sums -> states in the inputs' type
+cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s);              // sums -> states in the inputs' type
 
 // ---- device helpers ---------------------------------------------------------------------------------
 // The head's log decay: above 0 reads as 0 (no decay); -inf as the lowest value whose multiples stay finite.

@@ -71,7 +71,9 @@ xlstm_status_t xlstm_linattn_fwd(const xlstm_linattn_desc_t *desc, const void *q
     if (!outputs_disjoint(ins, outs)) return XLSTM_ERR_INVALID_ARG;
     const xlstm_status_t st = check_workspace(workspace, workspace_bytes, need);
     if (st != XLSTM_OK) return st;
-    if (cudaMemsetAsync(workspace, 0, 16, stream) != cudaSuccess) return XLSTM_ERR_CUDA;
+    // the fp32 kernels have no wait that can fail, and clear the status block themselves
+    if ((desc->T == 0 || desc->qkv_dtype == XLSTM_BF16) && cudaMemsetAsync(workspace, 0, 16, stream) != cudaSuccess)
+        return XLSTM_ERR_CUDA;
     if (desc->T == 0) return pass_state(C_out, C_in, sC, stream);
     LinAttnArgs a = pack(desc);
     a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.lens = lens; a.C0 = C_in; a.o = o; a.C1 = C_out;
@@ -119,7 +121,9 @@ xlstm_status_t xlstm_linattn_bwd(const xlstm_linattn_desc_t *desc, const void *q
     if (!outputs_disjoint(ins, outs)) return XLSTM_ERR_INVALID_ARG;
     const xlstm_status_t st = check_workspace(workspace, workspace_bytes, need);
     if (st != XLSTM_OK) return st;
-    if (cudaMemsetAsync(workspace, 0, 16, stream) != cudaSuccess) return XLSTM_ERR_CUDA;
+    // the fp32 kernels have no wait that can fail, and clear the status block themselves
+    if ((desc->T == 0 || desc->qkv_dtype == XLSTM_BF16) && cudaMemsetAsync(workspace, 0, 16, stream) != cudaSuccess)
+        return XLSTM_ERR_CUDA;
     if (desc->T == 0) return pass_state(dC_in, dC_out, sC, stream);
     LinAttnArgs a = pack(desc);
     a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.lens = lens; a.C0 = C_in;

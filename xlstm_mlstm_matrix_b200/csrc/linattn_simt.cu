@@ -10,8 +10,9 @@ namespace xlstm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPad = 68;      // row pitch of the transposed 64-wide tiles (4-float aligned, spreads banks)
-constexpr int kK = 32;        // inner-product columns staged at a time
+constexpr int kK = 32;            // inner-product columns of one step
+constexpr int kTile = 64 * kK;    // floats of a 64-row tile
+constexpr int kSeg = kSimtSegment;   // tokens of a segment: one output tile's rows
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
@@ -20,89 +21,140 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
 }
 
-// 64 rows x kK columns of a row-major matrix (nrows x ncols, rows `pitch` apart) into dst[column][row];
-// zeros outside it.
-__device__ __forceinline__ void stage_cols(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
+// 16 bytes to shared memory, asynchronously; zeros where !live (nothing is read then)
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A 64 x kK tile with its inner-product columns contiguous: float4 c of row r sits at column group
+// c ^ (r / 4 mod 8), so that the 16 rows 4 tx + j that a half warp reads fall on all banks twice.
+__device__ __forceinline__ int at(int r, int c) { return r * kK + 4 * (c ^ ((r >> 2) & 7)); }
+// R rows of a row-major matrix (nrows x ncols), columns col0 .. col0 + kK; zeros outside it
+template <int R>
+__device__ __forceinline__ void copy_tile(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
 #pragma unroll
-    for (int i = 0; i < 64 * kK / 4 / kThreads; ++i) {
-        const int e = threadIdx.x + i * kThreads, r = e & 63, c = (e >> 6) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < nrows && col0 + c < ncols) x = load4(src + (size_t)r * pitch + col0 + c);
-        dst[(c + 0) * kPad + r] = x.x;
-        dst[(c + 1) * kPad + r] = x.y;
-        dst[(c + 2) * kPad + r] = x.z;
-        dst[(c + 3) * kPad + r] = x.w;
+    for (int e = threadIdx.x; e < R * kK / 4; e += kThreads) {
+        const int r = e >> 3, c = e & 7;
+        const bool live = r < nrows && col0 + 4 * c < ncols;
+        copy16(dst + at(r, c), live ? src + (size_t)r * pitch + col0 + 4 * c : src, live);
     }
 }
-// kK rows x W columns into dst[row][column]; zeros outside.
-template <int W>
-__device__ __forceinline__ void stage_rows(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
+// R rows x W columns kept row-major; zeros outside the matrix
+template <int R, int W>
+__device__ __forceinline__ void copy_rows(float *dst, const float *src, size_t pitch, int nrows, int col0, int ncols) {
 #pragma unroll
-    for (int i = 0; i < kK * W / 4 / kThreads; ++i) {
-        const int e = threadIdx.x + i * kThreads, r = e / (W / 4), c = (e % (W / 4)) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < nrows && col0 + c < ncols) x = load4(src + (size_t)r * pitch + col0 + c);
-        *reinterpret_cast<float4 *>(dst + r * W + c) = x;
+    for (int e = threadIdx.x; e < R * W / 4; e += kThreads) {
+        const int r = e / (W / 4), c = (e % (W / 4)) * 4;
+        const bool live = r < nrows && col0 + c < ncols;
+        copy16(dst + r * W + c, live ? src + (size_t)r * pitch + col0 + c : src, live);
     }
 }
 
-// acc[n][i][j] += sum_k a[k][4 ty + i] b[k][64 n + 4 tx + j]
-template <int N>
-__device__ __forceinline__ void tile_fma(float (&acc)[N][4][4], const float *a, int lda, const float *b, int ldb, int ty,
-                                         int tx) {
-#pragma unroll 4
-    for (int k = 0; k < kK; ++k) {
-        const float4 av = *reinterpret_cast<const float4 *>(a + k * lda + 4 * ty);
-        const float ar[4] = {av.x, av.y, av.z, av.w};
+// acc[n][i][j] += sum_k a[M ty + i][k] b_n[4 tx + j][k]; b_n: N tiles one after another
+template <int M, int N>
+__device__ __forceinline__ void product_nt(float (&acc)[N][M][4], const float *a, const float *b, int ty, int tx) {
+#pragma unroll 2
+    for (int c = 0; c < kK / 4; ++c) {
+        float4 av[M];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const float4 bv = *reinterpret_cast<const float4 *>(b + k * ldb + 64 * n + 4 * tx);
-            const float br[4] = {bv.x, bv.y, bv.z, bv.w};
+        for (int i = 0; i < M; ++i) av[i] = load4(a + at(M * ty + i, c));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[n][i][j] = fmaf(ar[i], br[j], acc[n][i][j]);
+            for (int j = 0; j < 4; ++j) {
+                const float4 bv = load4(b + n * kTile + at(4 * tx + j, c));
+#pragma unroll
+                for (int i = 0; i < M; ++i)
+                    acc[n][i][j] = fmaf(av[i].x, bv.x, fmaf(av[i].y, bv.y, fmaf(av[i].z, bv.z, fmaf(av[i].w, bv.w, acc[n][i][j]))));
+            }
+    }
+}
+// acc[n][i][j] += sum_k a[M ty + i][k] b[k][64 n + 4 tx + j]
+template <int M, int N>
+__device__ __forceinline__ void product_nn(float (&acc)[N][M][4], const float *a, const float *b, int ty, int tx) {
+#pragma unroll 2
+    for (int c = 0; c < kK / 4; ++c) {
+        float ar[M][4];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float4 v = load4(a + at(M * ty + i, c));
+            ar[i][0] = v.x; ar[i][1] = v.y; ar[i][2] = v.z; ar[i][3] = v.w;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const float4 bv = load4(b + (4 * c + k) * 64 * N + 64 * n + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < M; ++i) {
+                    acc[n][i][0] = fmaf(ar[i][k], bv.x, acc[n][i][0]);
+                    acc[n][i][1] = fmaf(ar[i][k], bv.y, acc[n][i][1]);
+                    acc[n][i][2] = fmaf(ar[i][k], bv.z, acc[n][i][2]);
+                    acc[n][i][3] = fmaf(ar[i][k], bv.w, acc[n][i][3]);
+                }
+            }
     }
 }
 
-// ---- U_n = sum_s w_s z_s y_s^T of one segment, 64 z rows x 64 N y columns per block ------------------
-template <int N>
-__global__ void __launch_bounds__(kThreads) sums_kernel(LinStateP p, int ztiles, int ytiles) {
-    __shared__ __align__(16) float Zs[kK * 64];
-    __shared__ __align__(16) float Ys[kK * 64 * N];
-    __shared__ float ws[kK];
-    int id = blockIdx.x;
+// ---- U_n = sum_s w_s z_s y_s^T of one segment, 16 M z rows x 64 N y columns per block ------------------
+template <int M, int N>
+__global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ LinStates jobs) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int R = 16 * M;
+    float *Zs = sm, *Ys = Zs + kSeg * R;      // [token][R], [token][64 N]
+    __shared__ float ws[kSeg];
+    unsigned id;
+    const LinStateP &p = jobs.p[job_of_block(jobs, id)];
+    const int ytiles = (p.dqk + 64 * N - 1) / (64 * N), ztiles = (p.dv + R - 1) / R;
     const int yt = id % ytiles; id /= ytiles;
     const int zt = id % ztiles; id /= ztiles;
     const int n = id % p.nseg, bh = id / p.nseg;
-    const int len = seq_len(p.lens, bh / p.H, p.T), s0 = n * p.G, e = min(s0 + p.G, len);
-    if (s0 >= len) return;
-    const float ld = head_log_decay(p.log_decay, bh % p.H);
+    const int len = seq_len(p.lens, bh / p.H, p.T), s0 = n * kSeg, e = min(s0 + kSeg, len);
+    // the sum of the chain's last segment only enters the final state
+    if (s0 >= len || (!p.last && (p.rev ? n == 0 : e == len))) return;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int z0 = zt * 64, y0 = yt * 64 * N;
-    const float *z = static_cast<const float *>(p.z) + (size_t)bh * p.T * p.dv;
-    const float *y = static_cast<const float *>(p.y) + (size_t)bh * p.T * p.dqk;
-    float acc[N][4][4] = {};
-    for (int s = s0; s < e; s += kK) {
-        const int rows = min(kK, e - s);
-        __syncthreads();
-        if (tid < kK)
-            ws[tid] = tid < rows ? (p.rev ? p.scale * decay_pow(ld, s + tid - s0 + 1) : decay_pow(ld, e - 1 - s - tid))
-                                 : 0.f;
-        stage_rows<64>(Zs, z + (size_t)s * p.dv, p.dv, rows, z0, p.dv);
-        stage_rows<64 * N>(Ys, y + (size_t)s * p.dqk, p.dqk, rows, y0, p.dqk);
-        __syncthreads();
-        for (int i = tid; i < kK * 64; i += kThreads) Zs[i] *= ws[i / 64];
-        __syncthreads();
-        tile_fma<N>(acc, Zs, 64, Ys, 64 * N, ty, tx);
+    const int z0 = zt * R, y0 = yt * 64 * N;
+    copy_rows<kSeg, R>(Zs, static_cast<const float *>(p.z) + ((size_t)bh * p.T + s0) * p.dv, p.dv, e - s0, z0, p.dv);
+    copy_rows<kSeg, 64 * N>(Ys, static_cast<const float *>(p.y) + ((size_t)bh * p.T + s0) * p.dqk, p.dqk, e - s0, y0,
+                            p.dqk);
+    copies_commit();
+    if (tid < kSeg) {
+        const float ld = head_log_decay(p.log_decay, bh % p.H);
+        ws[tid] = s0 + tid < e ? (p.rev ? p.scale * decay_pow(ld, tid + 1) : decay_pow(ld, e - 1 - s0 - tid)) : 0.f;
+    }
+    copies_wait<0>();
+    __syncthreads();
+    float acc[N][M][4] = {};
+#pragma unroll 4
+    for (int s = 0; s < kSeg; ++s) {
+        float a[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) a[i] = ws[s] * Zs[s * R + M * ty + i];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const float4 b = load4(Ys + s * 64 * N + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                acc[c][i][0] = fmaf(a[i], b.x, acc[c][i][0]);
+                acc[c][i][1] = fmaf(a[i], b.y, acc[c][i][1]);
+                acc[c][i][2] = fmaf(a[i], b.z, acc[c][i][2]);
+                acc[c][i][3] = fmaf(a[i], b.w, acc[c][i][3]);
+            }
+        }
     }
     float *U = p.sums + ((size_t)bh * p.nseg + n) * p.dv * p.dqk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < M; ++i)
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-            const int r = z0 + 4 * ty + i, col = y0 + 64 * c + 4 * tx;
+            const int r = z0 + M * ty + i, col = y0 + 64 * c + 4 * tx;
             if (r < p.dv && col < p.dqk)
                 store4(U + (size_t)r * p.dqk + col,
                        make_float4(acc[c][i][0], acc[c][i][1], acc[c][i][2], acc[c][i][3]));
@@ -114,10 +166,12 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(LinStateP p, int ztiles,
 // memory (each element is read before it is written).  The factor l^{e_n-s_n} is held as two floats: over a
 // thousand segments one rounded factor would drift the oldest tokens' weight by a thousand of its roundings.
 template <typename S>
-__global__ void __launch_bounds__(kThreads) chain_kernel(LinStateP p, int per_head) {
-    const int bh = blockIdx.x / per_head;
+__global__ void __launch_bounds__(kThreads) chain_kernel(const __grid_constant__ LinStates jobs) {
+    unsigned id;
+    const LinStateP &p = jobs.p[job_of_block(jobs, id)];
     const size_t area = (size_t)p.dv * p.dqk;
-    const size_t el = ((size_t)(blockIdx.x % per_head) * kThreads + threadIdx.x) * 4;
+    const int per_head = (int)((area / 4 + kThreads - 1) / kThreads), bh = id / per_head;
+    const size_t el = ((size_t)(id % per_head) * kThreads + threadIdx.x) * 4;
     if (el >= area) return;
     const int len = seq_len(p.lens, bh / p.H, p.T), nseg = (len + p.G - 1) / p.G;
     const float ld = head_log_decay(p.log_decay, bh % p.H);
@@ -151,101 +205,112 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(LinStateP p, int per_he
     if (p.last) store4(p.last + (size_t)bh * area + el, c);
 }
 
-// ---- output tiles: 64 tokens x 64 N columns per block ---------------------------------------------------
+// ---- output tiles: 16 M of a segment's tokens x 64 N columns per block ---------------------------------------
+// Steps of kK inner-product columns, each step's operands copied while the one before is worked on: the
+// entering state's part (X against the state), the scores (X against Y), and the weighted scores against Z.
 template <int N>
-__global__ void __launch_bounds__(kThreads) tile_kernel(LinTileP p, int ttiles, int ztiles) {
+struct TileSmem {
+    static constexpr int STEP = (1 + N) * kTile;              // A tile, N B tiles
+    static constexpr int STEPS = 4;                            // 64, 96 or 160 KB: two blocks per SM at N = 1
+    static constexpr int BYTES = 4 * (STEPS * STEP + 2 * kTile + kSeg + 4);    // steps, scores, powers
+};
+template <int M, int N>
+__global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __grid_constant__ LinTiles jobs, int32_t *status) {
+    using S = TileSmem<N>;
     extern __shared__ __align__(16) float sm[];
-    float *Xs = sm;                    // [kK][kPad]
-    float *Ys = Xs + kK * kPad;        // [kK][kPad]
-    float *Ps = Ys + kK * kPad;        // [64][kPad]: weighted scores, token s by token t
-    float *Zs = Ps + 64 * kPad;        // [kK][64 N]
-    float *pw = Zs + kK * 64 * N;      // l^0 .. l^G
-    int id = blockIdx.x;
+    float *Ps = sm + S::STEPS * S::STEP;       // weighted scores, two tiles of kK tokens
+    float *pw = Ps + 2 * kTile;                // l^0 .. l^64
+    constexpr int R = 16 * M;
+    unsigned id;
+    const LinTileP &p = jobs.p[job_of_block(jobs, id)];
+    const int ztiles = (p.dz + 64 * N - 1) / (64 * N), ttiles = p.nseg * (kSeg / R);
     const int zt = id % ztiles; id /= ztiles;
-    const int tt = id % ttiles, bh = id / ttiles;
-    const int len = seq_len(p.lens, bh / p.H, p.T), t0 = tt * 64, z0 = zt * 64 * N;
+    const int tt = id % ttiles, bh = id / ttiles, n = tt * R / kSeg, r0 = tt * R % kSeg;    // rows r0 .. r0 + R of segment n
+    const int len = seq_len(p.lens, bh / p.H, p.T), t0 = n * kSeg, z0 = zt * 64 * N;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    // the call's last kernel: no wait of this path can fail
+    if (blockIdx.x == 0 && tid < 4) status[tid] = 0;
     float *out = static_cast<float *>(p.out) + (size_t)bh * p.T * p.dz;
-    float acc[N][4][4] = {};
-    if (t0 < len) {
+    float acc[N][M][4] = {};
+    if (t0 + r0 < len) {
         const float ld = head_log_decay(p.log_decay, bh % p.H);
-        const int n = t0 / p.G, s0 = n * p.G, e = min(s0 + p.G, len);
-        for (int i = tid; i <= p.G; i += kThreads) pw[i] = decay_pow(ld, i);
-        const float *x = static_cast<const float *>(p.x) + ((size_t)bh * p.T + t0) * p.dx;
-        const float *y = static_cast<const float *>(p.y) + (size_t)bh * p.T * p.dx;
-        const float *z = static_cast<const float *>(p.z) + (size_t)bh * p.T * p.dz;
-        const int xrows = min(64, len - t0);
-        __syncthreads();
-        // the entering state's part
+        const int e = min(t0 + kSeg, len), rows = e - t0;
+        const float *x = static_cast<const float *>(p.x) + ((size_t)bh * p.T + t0 + r0) * p.dx;
+        const float *y = static_cast<const float *>(p.y) + ((size_t)bh * p.T + t0) * p.dx;
+        const float *z = static_cast<const float *>(p.z) + ((size_t)bh * p.T + t0) * p.dz;
+        const float *state = static_cast<const float *>(p.states) + ((size_t)bh * p.nseg + n) * p.dx * p.dz;
         const bool entry = p.rev ? (e < len || p.has_init) : (n > 0 || p.has_init);
-        if (entry) {
-            const float *M = static_cast<const float *>(p.states) + ((size_t)bh * p.nseg + n) * p.dx * p.dz;
-            for (int k0 = 0; k0 < p.dx; k0 += kK) {
-                __syncthreads();
-                stage_cols(Xs, x, p.dx, xrows, k0, p.dx);
-                if (p.state_t) {
-                    stage_rows<64 * N>(Zs, M + (size_t)k0 * p.dz, p.dz, min(kK, p.dx - k0), z0, p.dz);
-                    __syncthreads();
-                    tile_fma<N>(acc, Xs, kPad, Zs, 64 * N, ty, tx);
+        const int nk = (p.dx + kK - 1) / kK, first = entry ? nk : 0, total = first + nk + 2;
+        auto fetch = [&](int st) {
+            if (st < total) {
+                float *A = sm + st % S::STEPS * S::STEP, *Bt = A + kTile;
+                if (st < first) {
+                    copy_tile<R>(A, x, p.dx, rows - r0, st * kK, p.dx);
+                    if (p.state_t)
+                        copy_rows<kK, 64 * N>(Bt, state + (size_t)st * kK * p.dz, p.dz, p.dx - st * kK, z0, p.dz);
+                    else
+#pragma unroll
+                        for (int c = 0; c < N; ++c)
+                            copy_tile<64>(Bt + c * kTile, state + (size_t)(z0 + 64 * c) * p.dx, p.dx, p.dz - z0 - 64 * c,
+                                          st * kK, p.dx);
+                } else if (st < first + nk) {
+                    copy_tile<R>(A, x, p.dx, rows - r0, (st - first) * kK, p.dx);
+                    copy_tile<64>(Bt, y, p.dx, rows, (st - first) * kK, p.dx);
                 } else {
-                    // [dz][dx]: 64 state rows at a time through the transposed tile
+                    const int h = st - first - nk;
+                    copy_rows<kK, 64 * N>(Bt, z + (size_t)h * kK * p.dz, p.dz, rows - h * kK, z0, p.dz);
+                }
+            }
+            copies_commit();
+        };
 #pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        if (c) __syncthreads();
-                        const int r0 = z0 + 64 * c;
-                        stage_cols(Ys, M + (size_t)r0 * p.dx, p.dx, p.dz - r0, k0, p.dx);
-                        __syncthreads();
-                        float part[1][4][4];
+        for (int st = 0; st < S::STEPS - 1; ++st) fetch(st);
+        for (int i = tid; i <= kSeg; i += kThreads) pw[i] = decay_pow(ld, i);
+        float sc[1][M][4] = {};
+        for (int st = 0; st < total; ++st) {
+            copies_wait<S::STEPS - 2>();
+            __syncthreads();
+            fetch(st + S::STEPS - 1);     // into the buffer of the step before, which every thread has left
+            const float *A = sm + st % S::STEPS * S::STEP, *Bt = A + kTile;
+            if (st < first) {
+                if (p.state_t) product_nn<M, N>(acc, A, Bt, ty, tx);
+                else product_nt<M, N>(acc, A, Bt, ty, tx);
+                if (st == first - 1) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) part[0][i / 4][i % 4] = acc[c][i / 4][i % 4];
-                        tile_fma<1>(part, Xs, kPad, Ys, kPad, ty, tx);
+                    for (int i = 0; i < M; ++i) {
+                        const int r = r0 + M * ty + i;
+                        const float rho = p.rev ? pw[max(rows - 1 - r, 0)] : p.scale * pw[r + 1];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[c][i / 4][i % 4] = part[0][i / 4][i % 4];
+                        for (int c = 0; c < N; ++c)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[c][i][j] *= rho;
                     }
                 }
-            }
+            } else if (st < first + nk) {
+                product_nt<M, 1>(sc, A, Bt, ty, tx);
+                if (st == first + nk - 1) {
+                    // token s = 4 tx + j is float4 tx of row t: tile tx / 8, column group tx mod 8
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + 4 * ty + i;
-                const float rho = t < len ? (p.rev ? pw[e - 1 - t] : p.scale * pw[t - s0 + 1]) : 0.f;
+                    for (int i = 0; i < M; ++i) {
+                        float w[4];
 #pragma unroll
-                for (int c = 0; c < N; ++c)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[c][i][j] *= rho;
-            }
-        }
-        // the segment's own tokens on the causal (or, reversed, the later) side
-        const int first = p.rev ? t0 : s0, stop = p.rev ? e : min(t0 + 64, e);
-        for (int b0 = first; b0 < stop; b0 += 64) {
-            const int yrows = min(64, e - b0);
-            float sc[1][4][4] = {};
-            for (int k0 = 0; k0 < p.dx; k0 += kK) {
-                __syncthreads();
-                stage_cols(Xs, x, p.dx, xrows, k0, p.dx);
-                stage_cols(Ys, y + (size_t)b0 * p.dx, p.dx, yrows, k0, p.dx);
-                __syncthreads();
-                tile_fma<1>(sc, Xs, kPad, Ys, kPad, ty, tx);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = t0 + 4 * ty + i, s = b0 + 4 * tx + j, far = p.rev ? s - t : t - s;
-                    Ps[(4 * tx + j) * kPad + 4 * ty + i] =
-                        (far >= 0 && s < e && t < e) ? p.scale * pw[far] * sc[0][i][j] : 0.f;
+                        for (int j = 0; j < 4; ++j) {
+                            const int t = r0 + M * ty + i, s = 4 * tx + j, far = p.rev ? s - t : t - s;
+                            w[j] = far >= 0 && s < rows ? p.scale * pw[far] * sc[0][i][j] : 0.f;
+                        }
+                        store4(Ps + (tx >> 3) * kTile + at(M * ty + i, tx & 7), make_float4(w[0], w[1], w[2], w[3]));
+                    }
                 }
-            for (int k0 = 0; k0 < 64; k0 += kK) {
-                __syncthreads();
-                stage_rows<64 * N>(Zs, z + (size_t)(b0 + k0) * p.dz, p.dz, yrows - k0, z0, p.dz);
-                __syncthreads();
-                tile_fma<N>(acc, Ps + k0 * kPad, kPad, Zs, 64 * N, ty, tx);
+            } else {
+                product_nn<M, N>(acc, Ps + (st - first - nk) * kTile, Bt, ty, tx);
             }
         }
+        copies_wait<0>();
     }
     // rows at or past the sequence's end hold zeros
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 4 * ty + i;
+    for (int i = 0; i < M; ++i) {
+        const int t = t0 + r0 + M * ty + i;
         if (t >= p.T) continue;
 #pragma unroll
         for (int c = 0; c < N; ++c) {
@@ -258,39 +323,79 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(LinTileP p, int ttiles, 
     }
 }
 
-int wide(int d) { return d > 128 ? 4 : d > 64 ? 2 : 1; }
+// Blocks hold 64 rows x 64 N columns.  Wide blocks read their rows fewer times, as long as a block per SM remains;
+// where not even one block of 64 x 64 per SM would run, a block holds 16 rows (a quarter of the work of each step
+// and four times the blocks).
+struct Shape {
+    int M, N;
+};
+Shape shape(int d, size_t blocks) {
+    if (blocks <= 148) return {1, 1};
+    int n = d > 128 ? 4 : d > 64 ? 2 : 1;
+    while (n > 1 && blocks / n < 148) n /= 2;
+    return {4, n};
+}
+size_t tiles64(int d) { return (size_t)(d + 63) / 64; }
 
-template <int N>
-cudaError_t tile_n(const LinTileP &p, cudaStream_t s) {
-    const int tt = (p.T + 63) / 64, zt = (p.dz + 64 * N - 1) / (64 * N);
-    const size_t smem = sizeof(float) * (2 * kK * kPad + 64 * kPad + kK * 64 * N + p.G + 1);
-    cudaError_t e = cudaFuncSetAttribute(tile_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename Jobs, typename Blocks>
+unsigned number_blocks(Jobs &jobs, Blocks blocks_of) {
+    size_t n = 0;
+    for (int j = 0; j < jobs.count; ++j) jobs.end[j] = (unsigned)(n += blocks_of(jobs.p[j]));
+    return (unsigned)n;
+}
+
+template <int M, int N>
+cudaError_t tile_mn(LinTiles &jobs, int32_t *status, cudaStream_t s) {
+    constexpr int smem = TileSmem<N>::BYTES;
+    const unsigned blocks = number_blocks(jobs, [](const LinTileP &p) {
+        return (size_t)p.B * p.H * p.nseg * (kSeg / (16 * M)) * ((p.dz + 64 * N - 1) / (64 * N));
+    });
+    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<M, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tile_kernel<N><<<(unsigned)((size_t)p.B * p.H * tt * zt), kThreads, smem, s>>>(p, tt, zt);
+    tile_kernel<M, N><<<blocks, kThreads, smem, s>>>(jobs, status);
+    return cudaGetLastError();
+}
+template <int M, int N>
+cudaError_t sums_mn(LinStates &jobs, cudaStream_t s) {
+    constexpr int smem = 4 * kSeg * (16 * M + 64 * N);
+    const unsigned blocks = number_blocks(jobs, [](const LinStateP &p) {
+        return (size_t)p.B * p.H * p.nseg * ((p.dv + 16 * M - 1) / (16 * M)) * ((p.dqk + 64 * N - 1) / (64 * N));
+    });
+    const cudaError_t e = cudaFuncSetAttribute(sums_kernel<M, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    sums_kernel<M, N><<<blocks, kThreads, smem, s>>>(jobs);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t linattn_sums_simt(const LinStateP &p, cudaStream_t s) {
-    const int N = wide(p.dqk), zt = (p.dv + 63) / 64, yt = (p.dqk + 64 * N - 1) / (64 * N);
-    const unsigned blocks = (unsigned)((size_t)p.B * p.H * p.nseg * zt * yt);
-    if (N == 1) sums_kernel<1><<<blocks, kThreads, 0, s>>>(p, zt, yt);
-    else if (N == 2) sums_kernel<2><<<blocks, kThreads, 0, s>>>(p, zt, yt);
-    else sums_kernel<4><<<blocks, kThreads, 0, s>>>(p, zt, yt);
-    return cudaGetLastError();
+cudaError_t linattn_sums_simt(LinStates jobs, cudaStream_t s) {
+    size_t blocks = 0;
+    for (int j = 0; j < jobs.count; ++j)
+        blocks += (size_t)jobs.p[j].B * jobs.p[j].H * jobs.p[j].nseg * tiles64(jobs.p[j].dv) * tiles64(jobs.p[j].dqk);
+    const Shape b = shape(jobs.p[0].dqk, blocks);
+    if (b.M == 1) return sums_mn<1, 1>(jobs, s);
+    return b.N == 1 ? sums_mn<4, 1>(jobs, s) : b.N == 2 ? sums_mn<4, 2>(jobs, s) : sums_mn<4, 4>(jobs, s);
 }
 
-cudaError_t linattn_tile_simt(const LinTileP &p, cudaStream_t s) {
-    const int N = wide(p.dz);
-    return N == 1 ? tile_n<1>(p, s) : N == 2 ? tile_n<2>(p, s) : tile_n<4>(p, s);
+cudaError_t linattn_tile_simt(LinTiles jobs, int32_t *status, cudaStream_t s) {
+    size_t blocks = 0;
+    int d = 512;
+    for (int j = 0; j < jobs.count; ++j) {
+        blocks += (size_t)jobs.p[j].B * jobs.p[j].H * jobs.p[j].nseg * tiles64(jobs.p[j].dz);
+        d = jobs.p[j].dz < d ? jobs.p[j].dz : d;
+    }
+    const Shape b = shape(d, blocks);
+    if (b.M == 1) return tile_mn<1, 1>(jobs, status, s);
+    return b.N == 1 ? tile_mn<4, 1>(jobs, status, s) : b.N == 2 ? tile_mn<4, 2>(jobs, status, s) : tile_mn<4, 4>(jobs, status, s);
 }
 
-cudaError_t linattn_chain(const LinStateP &p, bool bf16, cudaStream_t s) {
-    const int per_head = (int)(((size_t)p.dv * p.dqk / 4 + kThreads - 1) / kThreads);
-    const unsigned blocks = (unsigned)((size_t)p.B * p.H * per_head);
-    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(p, per_head);
-    else chain_kernel<float><<<blocks, kThreads, 0, s>>>(p, per_head);
+cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s) {
+    const unsigned blocks = number_blocks(jobs, [](const LinStateP &p) {
+        return (size_t)p.B * p.H * (((size_t)p.dv * p.dqk / 4 + kThreads - 1) / kThreads);
+    });
+    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(jobs);
+    else chain_kernel<float><<<blocks, kThreads, 0, s>>>(jobs);
     return cudaGetLastError();
 }
 
