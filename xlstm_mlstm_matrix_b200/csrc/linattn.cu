@@ -43,14 +43,17 @@ cudaError_t run_states(const LinAttnArgs &a, const LinStateP *p, int n, cudaStre
     LinStates sums{}, chains{};
     for (int i = 0; i < n; ++i) {
         if (p[i].nseg == 1 && !p[i].init && !p[i].last) continue;     // nothing enters, nothing is handed on
-        if (p[i].nseg > 1 || p[i].last) sums.p[sums.count++] = p[i];
+        const bool summed = p[i].nseg > 1 || p[i].last;
+        if (summed && bf16) {
+            const cudaError_t e = linattn_states_tc(p[i], a.status, s);
+            if (e != cudaSuccess) return e;
+            if (linattn_states_seq(p[i])) continue;
+        } else if (summed) {
+            sums.p[sums.count++] = p[i];
+        }
         chains.p[chains.count++] = p[i];
     }
-    cudaError_t e = cudaSuccess;
-    if (bf16)
-        for (int i = 0; e == cudaSuccess && i < sums.count; ++i) e = linattn_sums_tc(sums.p[i], a.status, s);
-    else if (sums.count)
-        e = linattn_sums_simt(sums, s);
+    const cudaError_t e = sums.count ? linattn_sums_simt(sums, s) : cudaSuccess;
     return e == cudaSuccess && chains.count ? linattn_chain(chains, bf16, s) : e;
 }
 

@@ -94,7 +94,9 @@ __device__ __forceinline__ int job_of_block(const LinJobs<P, MOST> &jobs, unsign
 constexpr int kSimtSegment = 64;                                              // the fp32 kernels' G
 cudaError_t linattn_sums_simt(LinStates jobs, cudaStream_t s);                     // fp32
 cudaError_t linattn_tile_simt(LinTiles jobs, int32_t *status, cudaStream_t s);     // clears status
-cudaError_t linattn_sums_tc(const LinStateP &p, int32_t *status, cudaStream_t s);     // bf16
+// bf16: the states at once where linattn_states_seq, else the sums for linattn_chain
+bool linattn_states_seq(const LinStateP &p);
+cudaError_t linattn_states_tc(const LinStateP &p, int32_t *status, cudaStream_t s);
 cudaError_t linattn_tile_tc(const LinTileP &p, int32_t *status, cudaStream_t s);
 cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s);              // sums -> states in the inputs' type
 

@@ -1,9 +1,23 @@
 // Device pieces of the tensor-core linear attention beside sm100.cuh and tc_common.cuh.
 #pragma once
 #include "tc_common.cuh"
+#include "tma_host.cuh"
 
 namespace xlstm {
 namespace {
+
+// Rank-3 fp32 tensor [z][y][x], boxes of 32 x box_y x 1 with 128-byte swizzle (make_tmap_3d_bf16's counterpart).
+inline bool make_tmap_3d_f32(CUtensorMap *m, const void *base, uint64_t x, uint64_t y, uint64_t z, uint32_t box_y) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {x, y, z};
+    cuuint64_t strides[2] = {x * 4, x * y * 4};
+    cuuint32_t box[3] = {32, box_y, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Stores a 3-D tile from 128-byte-swizzled shared memory; what lies past the tensor's extents is dropped.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
@@ -12,10 +26,27 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *s
                  "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until this thread's stores have read their shared memory.
-__device__ __forceinline__ void tma_store_wait() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Warp-wide: each thread reads 16 consecutive 32-bit columns of its own lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// l^n and l^m as two floats each: (l^n high, rest, l^m high, rest).  One rounded factor, applied once per segment,
+// would drift the oldest tokens' weight by a thousand of its roundings.
+__device__ __noinline__ float4 decay_factors(float ld, int n, int m) {
+    const double a = exp((double)ld * n), b = exp((double)ld * m);
+    return make_float4((float)a, (float)(a - (double)(float)a), (float)b, (float)(b - (double)(float)b));
 }
 
 // One warp brings R rows x 64 columns of a row-major bf16 matrix (ncols wide, from column col0) into a
@@ -25,7 +56,7 @@ template <int R>
 __device__ __noinline__ void load_box_rows(uint8_t *box, const __nv_bfloat16 *src, int ncols, int rows, int col0,
                                            int lane) {
 #pragma unroll 1
-    for (int e0 = 0; e0 < R * 8; e0 += 256) {
+    for (int e0 = 0; e0 < R * 8; e0 += 256) {   // R a multiple of 32
         uint4 v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -41,20 +72,24 @@ __device__ __noinline__ void load_box_rows(uint8_t *box, const __nv_bfloat16 *sr
     }
 }
 
-// w times eight bf16 values as a pair of bf16: hi = round(w v), lo = round(w v - hi).
-__device__ __forceinline__ void split_scaled(const uint4 &u, float w, uint4 &hi, uint4 &lo) {
+// w times eight bf16 values as three bf16 parts: the top 8 significand bits of w v, the next 8 and the last 8.  Cut off
+// rather than rounded, the parts of an fp32 value are exact (24 = 3 x 8) and cost bit operations only.
+__device__ __forceinline__ void split_scaled(const uint4 &u, float w, uint4 (&part)[3]) {
     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-    uint32_t h[4], l[4];
-    const float2 w2 = make_float2(w, w);
+    uint32_t o[3][4];
+    const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 x = __fmul2_rn(bf16x2_to_float2(in[i]), w2);
-        h[i] = pack_bf16x2(x.x, x.y);
-        const float2 f = bf16x2_to_float2(h[i]);
-        l[i] = pack_bf16x2(x.x - f.x, x.y - f.y);
+        float2 x = __fmul2_rn(bf16x2_to_float2(in[i]), w2);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+            o[k][i] = __byte_perm(a, b, 0x7632);
+            if (k < 2) x = __ffma2_rn(make_float2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)), minus, x);
+        }
     }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[k] = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
 }
 
 }  // namespace
