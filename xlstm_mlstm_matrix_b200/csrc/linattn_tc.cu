@@ -399,7 +399,9 @@ struct TileBars {   // indices into the barrier array
     static constexpr int X = 0, SCORES = 8, WEIGHTS = 9, PRODUCT = 10, ENTRY = 11, DONE = 12, RING = 13;   // RING: full, empty per stage
 };
 constexpr int kMaxStages = 7;
-constexpr int kTileTail = 132 * 4 + (TileBars::RING + 2 * kMaxStages) * 8 + 16;   // table, barriers, slots
+constexpr int kTab = 32 + 132 + 32;     // powers of the decay, room for masked columns on both sides
+constexpr int kTileTail = kTab * 4 + (TileBars::RING + 2 * kMaxStages) * 8 + 16;   // table, barriers, slots
+static_assert(7 * kUnit + kTileTail <= 113 * 1024, "two blocks share an SM");
 
 template <int NZ>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -409,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                    const int nkx, const int stages, int32_t *status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *ring = sm + nkx * kUnit;
-    float *tab = reinterpret_cast<float *>(ring + stages * kUnit);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(tab + 132);
+    float *tab = reinterpret_cast<float *>(ring + stages * kUnit) + 32;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(tab + kTab - 32);
     uint64_t *full = bar + TileBars::RING, *empty = full + stages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(empty + stages);
     Shared sh{reinterpret_cast<volatile int *>(tmem_slot + 1), status};
@@ -447,13 +449,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         *sh.abort_flag = 0;
         fence_mbar_init();
+        // the first loads need no one else: they are on their way while the block sets itself up
+        for (int c = 0; c < nkx; ++c) {
+            mbar_arrive_expect_tx(&bar[TileBars::X + c], kUnit);
+            tma_load_3d(sm + c * kUnit, &tmx, &bar[TileBars::X + c], 64 * c, t0, bh);
+            if (c < stages) {
+                mbar_arrive_expect_tx(&full[c], kUnit);
+                tma_load_3d(ring + c * kUnit, &tmy, &full[c], 64 * c, t0, bh);
+            }
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
     }
     // column c of a score tile at distance d tiles carries l^(128 (d - 1)) times tab[c] times the row's power
-    for (int i = tid; i <= 128; i += kThreads) tab[i] = decay_pow(ld, p.rev ? i : 128 - i);
+    for (int i = tid - 32; i < kTab - 32; i += kThreads)
+        tab[i] = i >= 0 && i <= 128 ? decay_pow(ld, p.rev ? i : 128 - i) : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -461,19 +473,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (warp == 0) {
         // ===================== loads =====================
-        int u = 0, xs = 0;  // ring units and chunks of X issued
+        int u = min(nkx, stages);   // ring units issued
         auto slot_free = [&](int st) {
             return u < stages || waitw(sh, &empty[st], (u / stages - 1) & 1, kWhereTileEmpty);
         };
-        auto y_tile = [&](int j, bool with_x) {
-            for (int c = 0; c < nkx; ++c) {
-                if (with_x) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&bar[TileBars::X + c], kUnit);
-                        tma_load_3d(sm + c * kUnit, &tmx, &bar[TileBars::X + c], 64 * c, t0, bh);
-                    }
-                    ++xs;
-                }
+        auto y_tile = [&](int j) {
+            for (int c = j ? 0 : u; c < nkx; ++c) {
                 const int st = u % stages;
                 if (!slot_free(st)) return false;
                 if (lane == 0) {
@@ -524,16 +529,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             return true;
         };
-        bool go = y_tile(0, true);
+        bool go = y_tile(0);
         if (go && entry) go = entry_state();
         if (go) go = z_tile(0);
-        for (int j = 1; go && j < nj; ++j) go = y_tile(j, false) && z_tile(j);
+        for (int j = 1; go && j < nj; ++j) go = y_tile(j) && z_tile(j);
         __syncwarp();
         if (lane == 0) {
             // every copy issued lands before shared memory is released
             for (int st = 0; st < stages; ++st)
                 if (u > st) drain_wait(&full[st], ((u - 1 - st) / stages) & 1);
-            for (int c = 0; c < xs; ++c) drain_wait(&bar[TileBars::X + c], 0);
+            for (int c = 0; c < nkx; ++c) drain_wait(&bar[TileBars::X + c], 0);
         }
     } else if (warp == 1) {
         // ===================== products =====================
@@ -614,39 +619,47 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             tc_fence_after();
             const int cols = p.rev ? min(128, e - (t0 + 128 * j)) : 128;     // live columns
-            // what the row contributes: scale times its power of the decay
-            const float f = j == 0 ? p.scale
-                                   : p.scale * decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
-            const int lo = j == 0 && p.rev ? r : 0, hi = j == 0 && !p.rev ? r + 1 : cols;
+            // Blocks of 32 columns against this warp's 32 rows.  Where all columns are on the past (future) side, a
+            // weight is the row's power times the column's; on the diagonal it is looked up by distance; masked
+            // scores are selected away, not multiplied, for they may be anything.
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int cb = 2 * half + b, c1 = 32 * cb, d = j > 0 ? 1 : p.rev ? cb - quarter : quarter - cb;
+                const uint32_t from = tm_s + lanes + c1, to = tm_s + lanes + 64 * half + 16 * b;
+                uint32_t pk[16];
+                if (d < 0) {
 #pragma unroll
-            for (int c0 = 0; c0 < 64; c0 += 32) {
+                    for (int i = 0; i < 16; ++i) pk[i] = 0;
+                    tmem_st16(to, pk);
+                    continue;
+                }
                 float x[32];
-                tmem_ld32(tm_s + lanes + 64 * half + c0, x);
+                tmem_ld32(from, x);
+                float f = p.scale;
+                if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
+                else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
                 tmem_wait_ld();
-                const int c1 = 64 * half + c0;
-                if (j > 0 && cols == 128) {
+                if (d > 0 && c1 + 32 <= cols) {
+                    const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
                     const float2 f2 = make_float2(f, f);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(tab + c1 + i);
+                        const float4 w = w4[i / 4];
                         const float2 a = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(w.x, w.y));
-                        const float2 b = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(w.z, w.w));
-                        x[i] = a.x; x[i + 1] = a.y; x[i + 2] = b.x; x[i + 3] = b.y;
+                        const float2 e2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(w.z, w.w));
+                        pk[i / 2] = pack_bf16x2(a.x, a.y);
+                        pk[i / 2 + 1] = pack_bf16x2(e2.x, e2.y);
                     }
                 } else {
-                    // masked columns are selected away, not multiplied: their scores may be anything
-                    const int off = j > 0 ? 0 : p.rev ? -r : 128 - r;
+                    // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
+                    const float *w = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
+                    const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = c1 + i;
-                        const float w = tab[min(max(c + off, 0), 128)];
-                        x[i] = c >= lo && c < hi ? x[i] * f * w : 0.f;
-                    }
+                    for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] * f * w[i] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
                 }
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                tmem_st16(tm_s + lanes + 64 * half + c0 / 2, pk);
+                tmem_st16(to, pk);
             }
             if (j == 0 && entry) {
                 if (!waitw(sh, &bar[TileBars::ENTRY], 0, kWhereTileEntry)) {
