@@ -6,12 +6,10 @@
 // state_tc_kernel: U_n = sum_s w_s z_s y_s^T, 128 z rows x NX y columns per block, 32 tokens a stage, chained over
 //   the segments where there are blocks enough.  The weighted rows w_s z_s enter as three bf16 parts: the final state
 //   leaves in fp32, one part would leave 2^-8 of each term and two 2^-16.
-// tile_tc_kernel: 128 tokens x NZ output columns per block.  X (the block's own rows) stays in shared memory;
-//   Y, Z and the entering state pass through a ring of 16 KB units.  Per 128 tokens of the segment the
-//   scores X Y^T land in tensor memory, eight warps weight them with powers of the decay and write them back
-//   as one bf16 copy (each rounding is relative to its own term), and the product with Z accumulates on top
-//   of the state's part.  The state's part is scaled by rho_t in tensor memory while the scores are formed.
-//   Two blocks share an SM, so that one's products run while the other waits for its weights.
+// tile_tc_kernel: 128 tokens x NZ output columns per tile.  The tile's own rows X stay in shared memory; Y, Z and the
+//   entering state pass through a ring of 16 KB units.  Per 128 tokens of the segment the scores X Y^T land in tensor
+//   memory, are weighted with powers of the decay and written back as one bf16 copy (each rounding is relative to its
+//   own term), and the product with Z accumulates on top of the state's part, scaled by rho_t in tensor memory.
 #include "linattn.cuh"
 #include "linattn_tc.cuh"
 #include "tma_host.cuh"
@@ -21,13 +19,13 @@ namespace {
 
 // Codes of the bounded waits in the status block.
 enum : int {
-    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206,
+    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206, kWhereSumOut = 207,
     kWhereTileEmpty = 211, kWhereTileX = 212, kWhereTileFull = 213, kWhereTileScores = 214, kWhereTileWeights = 215,
-    kWhereTileEntry = 216, kWhereTileProduct = 217, kWhereTileDone = 218,
+    kWhereTileEntry = 216, kWhereTileProduct = 217, kWhereTileDone = 218, kWhereTileTaken = 219, kWhereTileTable = 220,
+    kWhereTileOut = 221,
 };
 
-constexpr int kThreads = 320;       // TMA warp, MMA warp, eight warps of arithmetic
-constexpr int kMath = 8;            // arithmetic warps
+constexpr int kMath = 8;            // warps of one arithmetic role
 constexpr int kUnit = 16384;        // bytes of one ring unit
 
 // ---- entering states -----------------------------------------------------------------------------------
@@ -54,7 +52,7 @@ struct StateCfg {
     static constexpr int OUT = 128 * NX * (SEQ ? 2 : 4);        // what a store leaves from
     static constexpr int OFF_BAR = OFF_OUT + OUT;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_SCALED = 2 * STAGES, B_ACC = 3 * STAGES, B_TAKEN = B_ACC + 2,
-                         B_LAST = B_TAKEN + 2;
+                         B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_LAST = B_OUT_FREE + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * (B_LAST + 1);
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int STATE = NX;                            // state's first column (IN_TMEM)
@@ -111,6 +109,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             mbar_init(&bar[C::B_ACC + i], 1);
             mbar_init(&bar[C::B_TAKEN + i], 8);
         }
+        mbar_init(&bar[C::B_OUT_FULL], 8);
+        mbar_init(&bar[C::B_OUT_FREE], 1);
         mbar_init(&bar[C::B_LAST], 1);
         *sh.abort_flag = 0;
         fence_mbar_init();
@@ -260,23 +260,33 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         constexpr int CH = NX / 2;      // columns of this thread
         const uint32_t own_tm = tm + ((uint32_t)(32 * quarter) << 16) + half * CH;
         uint8_t *out = sm + C::OFF_OUT;
-        int g = 0;
-        bool go = true, staged = false;
-        // The thread that stores waits for its last store before the block writes the staging memory again.
-        auto staging_free = [&]() {
-            if (staged && tid == kFold) tma_store_wait();
-            staged = true;
-            named_barrier(1, 256);
-        };
-        auto store = [&](int slot, int z0, int y0) {
-            fence_proxy_async_smem();
-            named_barrier(1, 256);
-            constexpr int W = SEQ ? 64 : 32;    // columns of a box
+        int g = 0, stores = 0;
+        bool go = true;
+        // The staging memory is free once the store before has read it.  (Bounded waits, no block barrier: a warp that
+        // gave up would leave the others at one.)
+        const auto staging_free = [&]() {
             if (tid == kFold) {
-                for (int b = 0; b < NX / W; ++b)
-                    if (y0 + W * b < p.dqk) tma_store_3d(&tmo, out + b * 16384, y0 + W * b, z0, slot);
-                tma_store_commit();
+                if (stores > 0) tma_store_wait();
+                mbar_arrive(&bar[C::B_OUT_FREE]);
             }
+            return waitw(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
+        };
+        const auto store = [&](int slot, int z0, int y0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[C::B_OUT_FULL]);
+            if (warp == kFold / 32) {
+                if (!waitw(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
+                constexpr int W = SEQ ? 64 : 32;    // columns of a box
+                if (lane == 0) {
+                    for (int b = 0; b < NX / W; ++b)
+                        if (y0 + W * b < p.dqk) tma_store_3d(&tmo, out + b * 16384, y0 + W * b, z0, slot);
+                    tma_store_commit();
+                }
+                __syncwarp();
+            }
+            ++stores;
+            return true;
         };
         for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
             const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int k = 0; go && k < w.nseg; ++k) {
                     const int n = segment_of<SEQ>(p, w, k);
                     if (k > 0 || p.init) {      // the state entering segment n
-                        staging_free();
+                        if (!(go = staging_free())) break;
 #pragma unroll
                         for (int c0 = 0; c0 < CH; c0 += 32) {
                             float(&v)[32] = x[c0 / 32 % KEPT];
@@ -320,7 +330,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                                                pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
                             }
                         }
-                        store(w.bh * p.nseg + n, w.z0, w.y0);
+                        if (!(go = store(w.bh * p.nseg + n, w.z0, w.y0))) break;
                     }
                     if (k >= w.nm) break;
                     if (!waitw(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                staging_free();
+                if (!(go = staging_free())) break;
 #pragma unroll
                 for (int c0 = 0; c0 < CH; c0 += 32) {
                     float u[32];
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                 ++g;
-                store(w.bh * p.nseg + w.first, w.z0, w.y0);
+                go = store(w.bh * p.nseg + w.first, w.z0, w.y0);
             }
         }
         if (tid == kFold) tma_store_wait();
@@ -395,328 +405,476 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 }
 
 // ---- output tiles ---------------------------------------------------------------------------------------
-struct TileBars {   // indices into the barrier array
-    static constexpr int X = 0, SCORES = 8, WEIGHTS = 9, PRODUCT = 10, ENTRY = 11, DONE = 12, RING = 13;   // RING: full, empty per stage
-};
-constexpr int kMaxStages = 7;
+// One persistent block per SM.  Its work is a stream of units: 128 tokens x NZ columns of the output against 128 tokens
+// of the segment.  While eight warps weight the scores of unit k, the tensor core forms those of unit k + 1 (scores and
+// accumulators have two buffers each, all 512 columns), and eight more warps scale the entering state's part and read
+// finished tiles out.  Two warps issue the products, one the scores and the state's part, one the weighted scores
+// against Z: a wait and a commit per slot cost the issuing thread several hundred cycles, more than the eight products
+// of a slot take.
 constexpr int kTab = 32 + 132 + 32;     // powers of the decay, room for masked columns on both sides
-constexpr int kTileTail = kTab * 4 + (TileBars::RING + 2 * kMaxStages) * 8 + 16;   // table, barriers, slots
-static_assert(7 * kUnit + kTileTail <= 113 * 1024, "two blocks share an SM");
+constexpr int kTileThreads = 640;       // TMA, two of products, one idle; eight warps of weights; eight of scaling and read-out
+constexpr int kMaxRing = 10;
+struct TileBars {                       // indices into the barrier array; pairs are one per buffer
+    static constexpr int XFULL = 0, XFREE = 2, SCORES = 4, WEIGHTS = 6, PRODUCT = 8, ENTRY = 10, SCALED = 12, DONE = 14,
+                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, ZREADY = 23, RING = 25;
+};
+constexpr int kTileTail = 2 * kTab * 4 + (TileBars::RING + 2 * kMaxRing) * 8 + 16;
+
+// What a block has to know of one item: 128 tokens of a head, with the z tiles z .. z_end of its output.
+struct TileItem {
+    int bh, t0, len, n, s0, e, nj, z, z_end;
+    bool entry, some, live;      // some: an item at all; live: with tokens
+};
+// The k-th item of this block: rounds over the grid, turned by 37 blocks each so that a block meets every place
+// within the segments (whose tiles have between one and G / 128 units).
+template <int NZ>
+__device__ __forceinline__ bool tile_item(const LinTileP &p, int k, int items, int ttiles, int ztiles, int zgroup, TileItem &w) {
+    int id = k * gridDim.x + (blockIdx.x + 37u * k) % gridDim.x;
+    w.some = w.live = false;
+    if (id >= items) return k * (int)gridDim.x < items;     // the last round's idle blocks
+    const int zgroups = (ztiles + zgroup - 1) / zgroup;
+    w.z = id % zgroups * zgroup;
+    w.z_end = min(w.z + zgroup, ztiles);
+    id /= zgroups;
+    w.t0 = id % ttiles * 128;
+    w.bh = id / ttiles;
+    w.len = seq_len(p.lens, w.bh / p.H, p.T);
+    w.n = w.t0 / p.G;
+    w.s0 = w.n * p.G;
+    w.e = min(w.s0 + p.G, w.len);
+    w.entry = p.rev ? (w.e < w.len || p.has_init) : (w.n > 0 || p.has_init);
+    // 128-token score tiles on this tile's past (future) side, its own first
+    w.nj = p.rev ? (w.e - w.t0 + 127) / 128 : (w.t0 - w.s0) / 128 + 1;
+    w.some = true;
+    w.live = w.t0 < w.len;
+    return true;
+}
+
+// Where a role stands in the ring: the slot, and the parity of its current pass.
+struct RingAt {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 template <int NZ>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     tile_tc_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmy,
                    const __grid_constant__ CUtensorMap tmz, const __grid_constant__ CUtensorMap tms,
-                   const __grid_constant__ CUtensorMap tmo, const LinTileP p, const int ttiles, const int ztiles,
-                   const int nkx, const int stages, int32_t *status) {
+                   const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinTileP p, const int items,
+                   const int ttiles, const int ztiles, const int zgroup, const int nkx, const int nx, const int stages,
+                   const int slot_bytes, int32_t *status) {
     extern __shared__ __align__(1024) uint8_t sm[];
-    uint8_t *ring = sm + nkx * kUnit;
-    float *tab = reinterpret_cast<float *>(ring + stages * kUnit) + 32;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(tab + kTab - 32);
+    uint8_t *ring = sm + nx * nkx * kUnit, *out = ring + stages * slot_bytes;
+    float *tabs = reinterpret_cast<float *>(out + NZ * 256) + 32;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(tabs + 2 * kTab - 32);
     uint64_t *full = bar + TileBars::RING, *empty = full + stages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(empty + stages);
     Shared sh{reinterpret_cast<volatile int *>(tmem_slot + 1), status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int id = blockIdx.x;
-    const int z0 = id % ztiles * NZ; id /= ztiles;
-    const int t0 = id % ttiles * 128, bh = id / ttiles;
-    const int len = seq_len(p.lens, bh / p.H, p.T);
-    if (t0 >= len) {   // behind the sequence: zeros
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)bh * p.T + t0) * p.dz;
-        for (int i = tid; i < 128 * (NZ / 8); i += kThreads) {
-            const int r = i / (NZ / 8), c = z0 + i % (NZ / 8) * 8;
-            if (t0 + r < p.T && c < p.dz) *reinterpret_cast<uint4 *>(out + (size_t)r * p.dz + c) = make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
-    const int n = t0 / p.G, s0 = n * p.G, e = min(s0 + p.G, len);
-    const float ld = head_log_decay(p.log_decay, bh % p.H);
-    const bool entry = p.rev ? (e < len || p.has_init) : (n > 0 || p.has_init);
-    // 128-token score tiles on this tile's past (future) side, its own first
-    const int nj = p.rev ? (e - t0 + 127) / 128 : (t0 - s0) / 128 + 1;
     const int dir = p.rev ? 128 : -128;
 
     if (tid == 0) {
-        for (int i = 0; i < nkx; ++i) mbar_init(&bar[TileBars::X + i], 1);
-        mbar_init(&bar[TileBars::SCORES], 1);
-        mbar_init(&bar[TileBars::WEIGHTS], kMath);
-        mbar_init(&bar[TileBars::PRODUCT], 1);
-        mbar_init(&bar[TileBars::ENTRY], 1);
-        mbar_init(&bar[TileBars::DONE], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[TileBars::XFULL + i], 1);
+            mbar_init(&bar[TileBars::XFREE + i], 1);
+            mbar_init(&bar[TileBars::ZREADY + i], 1);
+            mbar_init(&bar[TileBars::SCORES + i], 1);
+            mbar_init(&bar[TileBars::WEIGHTS + i], kMath);
+            mbar_init(&bar[TileBars::PRODUCT + i], 1);
+            mbar_init(&bar[TileBars::ENTRY + i], 1);
+            mbar_init(&bar[TileBars::SCALED + i], kMath);
+            mbar_init(&bar[TileBars::DONE + i], 1);
+            mbar_init(&bar[TileBars::TAKEN + i], kMath);
+        }
+        mbar_init(&bar[TileBars::TABLE], kMath);
+        mbar_init(&bar[TileBars::OUT_FULL], kMath);
+        mbar_init(&bar[TileBars::OUT_FREE], 1);
+        mbar_init(&bar[TileBars::LAST], 1);
+        mbar_init(&bar[TileBars::LAST + 1], 1);
         for (int i = 0; i < stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         *sh.abort_flag = 0;
         fence_mbar_init();
-        // the first loads need no one else: they are on their way while the block sets itself up
-        for (int c = 0; c < nkx; ++c) {
-            mbar_arrive_expect_tx(&bar[TileBars::X + c], kUnit);
-            tma_load_3d(sm + c * kUnit, &tmx, &bar[TileBars::X + c], 64 * c, t0, bh);
-            if (c < stages) {
-                mbar_arrive_expect_tx(&full[c], kUnit);
-                tma_load_3d(ring + c * kUnit, &tmy, &full[c], 64 * c, t0, bh);
-            }
-        }
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 256);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    // column c of a score tile at distance d tiles carries l^(128 (d - 1)) times tab[c] times the row's power
-    for (int i = tid - 32; i < kTab - 32; i += kThreads)
-        tab[i] = i >= 0 && i <= 128 ? decay_pow(ld, p.rev ? i : 128 - i) : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = *tmem_slot, tm_s = tm + 128;
+    const uint32_t tm = *tmem_slot;
+    const auto scores_at = [&](int k) { return tm + 256 + 128 * (k & 1); };
+    const auto acc_at = [&](int i) { return tm + 128 * (i & 1); };
+    TileItem w;
 
     if (warp == 0) {
         // ===================== loads =====================
-        int u = min(nkx, stages);   // ring units issued
-        auto slot_free = [&](int st) {
-            return u < stages || waitw(sh, &empty[st], (u / stages - 1) & 1, kWhereTileEmpty);
-        };
-        auto y_tile = [&](int j) {
-            for (int c = j ? 0 : u; c < nkx; ++c) {
-                const int st = u % stages;
-                if (!slot_free(st)) return false;
+        int u = 0, xi = 0;      // ring slots and items' X issued
+        const auto run = [&]() {
+            RingAt at;
+            const auto next = [&](int &st) {
+                st = at.slot;
+                const bool ok = u < stages || waitw(sh, &empty[st], at.phase ^ 1, kWhereTileEmpty);
+                at.next(stages);
+                return ok;
+            };
+            for (int k = 0; tile_item<NZ>(p, k, items, ttiles, ztiles, zgroup, w); ++k) {
+                if (!w.live) continue;
+                const int xb = xi % nx;
+                if (xi >= nx && !waitw(sh, &bar[TileBars::XFREE + xb], (xi / nx - 1) & 1, kWhereTileX)) return;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], kUnit);
-                    tma_load_3d(ring + st * kUnit, &tmy, &full[st], 64 * c, t0 + j * dir, bh);
+                    mbar_arrive_expect_tx(&bar[TileBars::XFULL + xb], nkx * kUnit);
+                    for (int c = 0; c < nkx; ++c)
+                        tma_load_3d(sm + (xb * nkx + c) * kUnit, &tmx, &bar[TileBars::XFULL + xb], 64 * c, w.t0, w.bh);
                 }
-                ++u;
+                ++xi;
+                for (int z = w.z; z < w.z_end; ++z)
+                    for (int j = 0; j < w.nj; ++j) {
+                        const int t = w.t0 + j * dir;
+                        int st;
+                        for (int c = 0; c < nkx; c += 2, ++u) {
+                            if (!next(st)) return;
+                            if (lane == 0) {
+                                const int two = c + 1 < nkx;
+                                mbar_arrive_expect_tx(&full[st], (1 + two) * kUnit);
+                                for (int h = 0; h <= two; ++h)
+                                    tma_load_3d(ring + st * slot_bytes + h * kUnit, &tmy, &full[st], 64 * (c + h), t, w.bh);
+                            }
+                        }
+                        for (int c = 0; j == 0 && w.entry && c < nkx; c += 2, ++u) {
+                            if (!next(st)) return;
+                            if (lane == 0) {
+                                const int slot = w.bh * p.nseg + w.n, two = c + 1 < nkx;
+                                if (p.state_t) {    // 128 (64) state rows, their columns in boxes of 64
+                                    mbar_arrive_expect_tx(&full[st], NZ / 64 * 64 * 128 * (1 + two));
+                                    for (int b = 0; b < NZ / 64; ++b)
+                                        for (int h = 0; h <= two; ++h)
+                                            tma_load_3d(ring + st * slot_bytes + b * kUnit + h * 8192, &tms, &full[st],
+                                                        z * NZ + 64 * b, 64 * (c + h), slot);
+                                } else {
+                                    mbar_arrive_expect_tx(&full[st], NZ * 128 * (1 + two));
+                                    for (int h = 0; h <= two; ++h)
+                                        tma_load_3d(ring + st * slot_bytes + h * kUnit, &tms, &full[st], 64 * (c + h), z * NZ, slot);
+                                }
+                            }
+                        }
+                        if (!next(st)) return;
+                        if (p.lens && t + 128 > w.len) {
+                            // the tile the sequence ends in: rows behind its end read as zeros, whatever is there
+                            for (int b = 0; b < NZ / 64; ++b)
+                                load_box_rows<128>(ring + st * slot_bytes + b * kUnit,
+                                                   static_cast<const __nv_bfloat16 *>(p.z) + ((size_t)w.bh * p.T + t) * p.dz,
+                                                   p.dz, w.len - t, z * NZ + 64 * b, lane);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&full[st]);
+                        } else if (lane == 0) {
+                            mbar_arrive_expect_tx(&full[st], NZ / 64 * kUnit);
+                            for (int b = 0; b < NZ / 64; ++b)
+                                tma_load_3d(ring + st * slot_bytes + b * kUnit, &tmz, &full[st], z * NZ + 64 * b, t, w.bh);
+                        }
+                        __syncwarp();
+                        ++u;
+                    }
             }
-            return true;
         };
-        auto entry_state = [&]() {
-            const int slot = bh * p.nseg + n;
-            for (int c = 0; c < nkx; ++c) {
-                const int st = u % stages;
-                if (!slot_free(st)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], NZ * 128);
-                    if (p.state_t)
-                        for (int b = 0; b < NZ / 64; ++b)
-                            tma_load_3d(ring + st * kUnit + 8192 * b, &tms, &full[st], z0 + 64 * b, 64 * c, slot);
-                    else
-                        tma_load_3d(ring + st * kUnit, &tms, &full[st], 64 * c, z0, slot);
-                }
-                ++u;
-            }
-            return true;
-        };
-        auto z_tile = [&](int j) {
-            constexpr int R = NZ == 128 ? 64 : 128;     // tokens of a unit
-            for (int h = 0; h < 128 / R; ++h) {
-                const int st = u % stages, t = t0 + j * dir + R * h;
-                if (!slot_free(st)) return false;
-                if (p.lens && t + R > len) {
-                    // the tile the sequence ends in: rows behind its end read as zeros, whatever is there
-                    for (int b = 0; b < NZ / 64; ++b)
-                        load_box_rows<R>(ring + st * kUnit + 8192 * b,
-                                         static_cast<const __nv_bfloat16 *>(p.z) + ((size_t)bh * p.T + t) * p.dz, p.dz,
-                                         len - t, z0 + 64 * b, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[st]);
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], kUnit);
-                    for (int b = 0; b < NZ / 64; ++b)
-                        tma_load_3d(ring + st * kUnit + 8192 * b, &tmz, &full[st], z0 + 64 * b, t, bh);
-                }
-                ++u;
-            }
-            return true;
-        };
-        bool go = y_tile(0);
-        if (go && entry) go = entry_state();
-        if (go) go = z_tile(0);
-        for (int j = 1; go && j < nj; ++j) go = y_tile(j) && z_tile(j);
+        run();
         __syncwarp();
         if (lane == 0) {
             // every copy issued lands before shared memory is released
             for (int st = 0; st < stages; ++st)
                 if (u > st) drain_wait(&full[st], ((u - 1 - st) / stages) & 1);
-            for (int c = 0; c < nkx; ++c) drain_wait(&bar[TileBars::X + c], 0);
+            for (int b = 0; b < nx; ++b)
+                if (xi > b) drain_wait(&bar[TileBars::XFULL + b], ((xi - 1 - b) / nx) & 1);
         }
     } else if (warp == 1) {
-        // ===================== products =====================
-        if (lane == 0) {
-            constexpr uint32_t id_s = make_idesc(128, 128, kFmtBF16, kFmtBF16, 0, 0);
-            constexpr uint32_t id_pz = make_idesc(128, NZ, kFmtBF16, kFmtBF16, 0, 1);
-            const uint32_t id_e = make_idesc(128, NZ, kFmtBF16, kFmtBF16, 0, p.state_t);
-            const uint64_t x = smem_desc_sw128(smem_u32(sm), 16, 1024);
-            int u = 0;
-            bool go = true;
-            auto unit = [&](uint32_t &addr) {      // waits for the next ring unit
-                const int st = u % stages;
-                if (!wait1(sh, &full[st], (u / stages) & 1, kWhereTileFull)) return false;
-                tc_fence_after();
-                addr = smem_u32(ring + st * kUnit);
-                return true;
-            };
-            auto release = [&]() { tc_commit(&empty[u++ % stages]); };
-            for (int j = 0; go && j < nj; ++j) {
-                // the weighted scores of the tile before share the columns
-                if (j > 0 && !wait1(sh, &bar[TileBars::PRODUCT], (j - 1) & 1, kWhereTileProduct)) { go = false; break; }
-                for (int c = 0; go && c < nkx; ++c) {
-                    uint32_t a;
-                    go = (j > 0 || wait1(sh, &bar[TileBars::X + c], 0, kWhereTileX)) && unit(a);
-                    if (!go) break;
-                    const uint64_t y = smem_desc_sw128(a, 16, 1024);
+        // ===================== scores, entering state's part =====================
+        // The whole warp walks the work, so that descriptors stay uniform; one lane issues.
+        constexpr uint32_t id_s = make_idesc(128, 128, kFmtBF16, kFmtBF16, 0, 0);
+        const uint32_t id_e = make_idesc(128, NZ, kFmtBF16, kFmtBF16, 0, p.state_t);
+        const bool leader = elect_one();
+        const auto run = [&]() {
+            RingAt at;
+            int xi = 0, k = 0, i = 0;           // items, units and tiles so far
+            for (int r = 0; tile_item<NZ>(p, r, items, ttiles, ztiles, zgroup, w); ++r) {
+                if (!w.live) continue;
+                const int xb = nx == 2 ? xi & 1 : 0;
+                if (!waitw(sh, &bar[TileBars::XFULL + xb], (nx == 2 ? xi >> 1 : xi) & 1, kWhereTileX)) return;
+                const uint64_t x = smem_desc_sw128(smem_u32(sm + xb * nkx * kUnit), 16, 1024);
+                for (int z = w.z; z < w.z_end; ++z, ++i)
+                    for (int j = 0; j < w.nj; ++j, ++k) {
+                        // the weighted scores of two units ago share the columns
+                        if (k >= 2 && !waitw(sh, &bar[TileBars::PRODUCT + (k & 1)], (k / 2 - 1) & 1, kWhereTileProduct)) return;
+                        tc_fence_after();
+                        const uint32_t sc = scores_at(k), acc = acc_at(i);
+                        for (int c = 0; c < nkx; c += 2) {
+                            if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
+                            const uint64_t y = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), 16, 1024);
+                            const uint64_t xc = x + (uint32_t)(c * kUnit >> 4);
+                            if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(tm_s, x + (uint32_t)((c * kUnit + 32 * ks) >> 4), y + 2 * ks, id_s, c > 0 || ks > 0);
-                    release();
-                }
-                if (!go) break;
-                tc_commit(&bar[TileBars::SCORES]);
-                if (j == 0 && entry) {
-                    for (int c = 0; go && c < nkx; ++c) {
-                        uint32_t a;
-                        if (!(go = unit(a))) break;
-                        const uint64_t s = p.state_t ? smem_desc_sw128(a, 8192, 1024) : smem_desc_sw128(a, 16, 1024);
-                        const uint32_t step = p.state_t ? 2048 >> 4 : 2;
+                                for (int ks = 0; ks < 4; ++ks) mma_f16_ss(sc, xc + 2 * ks, y + 2 * ks, id_s, c > 0 || ks > 0);
+                                if (c + 1 < nkx)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tm, x + (uint32_t)((c * kUnit + 32 * ks) >> 4), s + ks * step, id_e, c > 0 || ks > 0);
-                        release();
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        mma_f16_ss(sc, xc + (kUnit >> 4) + 2 * ks, y + (kUnit >> 4) + 2 * ks, id_s, 1);
+                                tc_commit(&empty[at.slot]);
+                            }
+                            at.next(stages);
+                        }
+                        if (leader) tc_commit(&bar[TileBars::SCORES + (k & 1)]);
+                        if (j == 0) {
+                            // the tile that used the accumulator before has been read out
+                            if (i >= 2 && !waitw(sh, &bar[TileBars::TAKEN + (i & 1)], (i / 2 - 1) & 1, kWhereTileTaken)) return;
+                            tc_fence_after();
+                            // K-major state: 32 bytes a step, the next 64 columns one box on; MN-major: 16 rows a step
+                            const uint32_t step = p.state_t ? 2048 >> 4 : 2, next64 = p.state_t ? 8192 >> 4 : kUnit >> 4;
+                            for (int c = 0; w.entry && c < nkx; c += 2) {
+                                if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
+                                const uint64_t s = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), p.state_t ? kUnit : 16, 1024);
+                                const uint64_t xc = x + (uint32_t)(c * kUnit >> 4);
+                                if (leader) {
+#pragma unroll
+                                    for (int ks = 0; ks < 4; ++ks) mma_f16_ss(acc, xc + 2 * ks, s + ks * step, id_e, c > 0 || ks > 0);
+                                    if (c + 1 < nkx)
+#pragma unroll
+                                        for (int ks = 0; ks < 4; ++ks)
+                                            mma_f16_ss(acc, xc + (kUnit >> 4) + 2 * ks, s + next64 + ks * step, id_e, 1);
+                                    tc_commit(&empty[at.slot]);
+                                }
+                                at.next(stages);
+                            }
+                            if (leader) tc_commit(&bar[TileBars::ENTRY + (i & 1)]);
+                        }
+                        if (leader && j == w.nj - 1 && z == w.z_end - 1) tc_commit(&bar[TileBars::XFREE + xb]);
+                        // Z's slot goes to the other warp.  Its arrival is seen here all the same, and passed on: a warp
+                        // that skipped a phase of a slot could take the one before it for the next one.
+                        if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
+                        at.next(stages);
+                        if (leader) mbar_arrive(&bar[TileBars::ZREADY + (k & 1)]);
                     }
-                    if (!go) break;
-                    tc_commit(&bar[TileBars::ENTRY]);
-                }
-                if (!(go = wait1(sh, &bar[TileBars::WEIGHTS], j & 1, kWhereTileWeights))) break;
-                tc_fence_after();
-                constexpr int R = NZ == 128 ? 64 : 128;
-#pragma unroll
-                for (int h = 0; h < 128 / R; ++h) {
-                    uint32_t a;
-                    if (!(go = unit(a))) break;
-                    const uint64_t z = smem_desc_sw128(a, 8192, 1024);
-#pragma unroll
-                    for (int ks = 0; ks < R / 16; ++ks) {
-                        const int k = h * (R / 16) + ks;     // 16 tokens: 8 packed columns, 64 apart per half tile
-                        mma_f16_ts(tm, tm_s + 64 * (k / 4) + 8 * (k % 4), z + (uint32_t)(ks * 2048 >> 4), id_pz,
-                                   entry || j > 0 || k > 0);
-                    }
-                    release();
-                }
-                if (go) tc_commit(&bar[TileBars::PRODUCT]);
+                ++xi;
             }
-            tc_commit(&bar[TileBars::DONE]);
-            drain_wait(&bar[TileBars::DONE], 0);
+        };
+        run();
+        __syncwarp();
+        if (leader) {
+            tc_commit(&bar[TileBars::LAST]);     // nothing in flight when tensor memory is freed
+            drain_wait(&bar[TileBars::LAST], 0);
         }
-    } else {
-        // ===================== weights, read-out =====================
-        const int quarter = warp & 3, half = (warp - 2) >> 2, r = 32 * quarter + lane, t = t0 + r;
-        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        bool alive = true;
-        for (int j = 0; j < nj; ++j) {
-            if (!waitw(sh, &bar[TileBars::SCORES], j & 1, kWhereTileScores)) {
-                alive = false;
-                break;
-            }
-            tc_fence_after();
-            const int cols = p.rev ? min(128, e - (t0 + 128 * j)) : 128;     // live columns
-            // Blocks of 32 columns against this warp's 32 rows.  Where all columns are on the past (future) side, a
-            // weight is the row's power times the column's; on the diagonal it is looked up by distance; masked
-            // scores are selected away, not multiplied, for they may be anything.
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                const int cb = 2 * half + b, c1 = 32 * cb, d = j > 0 ? 1 : p.rev ? cb - quarter : quarter - cb;
-                const uint32_t from = tm_s + lanes + c1, to = tm_s + lanes + 64 * half + 16 * b;
-                uint32_t pk[16];
-                if (d < 0) {
+    } else if (warp == 2) {
+        // ===================== weighted scores against Z =====================
+        constexpr uint32_t id_pz = make_idesc(128, NZ, kFmtBF16, kFmtBF16, 0, 1);
+        const bool leader = elect_one();
+        const int nys = (nkx + 1) / 2;
+        const auto run = [&]() {
+            RingAt at;
+            int k = 0, i = 0;
+            for (int r = 0; tile_item<NZ>(p, r, items, ttiles, ztiles, zgroup, w); ++r) {
+                if (!w.live) continue;
+                for (int z = w.z; z < w.z_end; ++z, ++i)
+                    for (int j = 0; j < w.nj; ++j, ++k) {
+                        for (int c = j == 0 && w.entry ? 2 * nys : nys; c > 0; --c) at.next(stages);     // Y's and the state's slots
+                        if (j == 0 && !waitw(sh, &bar[TileBars::SCALED + (i & 1)], (i >> 1) & 1, kWhereTileEntry)) return;
+                        if (!waitw(sh, &bar[TileBars::ZREADY + (k & 1)], (k >> 1) & 1, kWhereTileFull)) return;
+                        if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
+                        if (!waitw(sh, &bar[TileBars::WEIGHTS + (k & 1)], (k >> 1) & 1, kWhereTileWeights)) return;
+                        tc_fence_after();
+                        const uint64_t zd = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), kUnit, 1024);
+                        const uint32_t acc = acc_at(i), ps = scores_at(k);
+                        if (leader) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[i] = 0;
-                    tmem_st16(to, pk);
+                            for (int q = 0; q < 8; ++q)     // 16 tokens: 8 packed columns, 64 apart per half tile
+                                mma_f16_ts(acc, ps + 64 * (q / 4) + 8 * (q % 4), zd + (uint32_t)(q * 2048 >> 4), id_pz,
+                                           w.entry || j > 0 || q > 0);
+                            tc_commit(&empty[at.slot]);
+                            tc_commit(&bar[TileBars::PRODUCT + (k & 1)]);
+                            if (j == w.nj - 1) tc_commit(&bar[TileBars::DONE + (i & 1)]);
+                        }
+                        at.next(stages);
+                    }
+            }
+        };
+        run();
+        __syncwarp();
+        if (leader) {
+            tc_commit(&bar[TileBars::LAST + 1]);
+            drain_wait(&bar[TileBars::LAST + 1], 0);
+        }
+    } else if (warp == 3) {
+        // idle: the arithmetic warps start at a multiple of four
+    } else if (warp < 4 + kMath) {
+        // ===================== weights =====================
+        const int quarter = warp & 3, half = (warp - 4) >> 2, r = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const auto run = [&]() {
+            int k = 0, xi = 0;
+            for (int it = 0; tile_item<NZ>(p, it, items, ttiles, ztiles, zgroup, w); ++it) {
+                if (!w.live) continue;
+                const float ld = head_log_decay(p.log_decay, w.bh % p.H);
+                // Column c of a score tile at distance d tiles carries l^(128 (d - 1)) times tab[c] times the row's power.
+                // A warp that writes this item's table has seen all warps write the one before, and so leave the one
+                // before that, whose place this is.
+                float *tab = tabs + (xi & 1) * kTab;
+                for (int c = tid - 128 - 32; c < kTab - 32; c += 32 * kMath)
+                    tab[c] = c >= 0 && c <= 128 ? decay_pow(ld, p.rev ? c : 128 - c) : 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[TileBars::TABLE]);
+                if (!waitw(sh, &bar[TileBars::TABLE], xi & 1, kWhereTileTable)) return;
+                ++xi;
+                for (int z = w.z; z < w.z_end; ++z)
+                    for (int j = 0; j < w.nj; ++j, ++k) {
+                        const uint32_t tm_s = scores_at(k);
+                        const int cols = p.rev ? min(128, w.e - (w.t0 + 128 * j)) : 128;     // live columns
+                        if (!waitw(sh, &bar[TileBars::SCORES + (k & 1)], (k >> 1) & 1, kWhereTileScores)) return;
+                        tc_fence_after();
+                        // Blocks of 32 columns against this warp's 32 rows.  Where all columns are on the past (future)
+                        // side, a weight is the row's power times the column's; on the diagonal it is looked up by
+                        // distance; masked scores are selected away, not multiplied, for they may be anything.
+#pragma unroll 1
+                        for (int b = 0; b < 2; ++b) {
+                            const int cb = 2 * half + b, c1 = 32 * cb, d = j > 0 ? 1 : p.rev ? cb - quarter : quarter - cb;
+                            const uint32_t from = tm_s + lanes + c1, to = tm_s + lanes + 64 * half + 16 * b;
+                            uint32_t pk[16];
+                            if (d < 0) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) pk[i] = 0;
+                                tmem_st16(to, pk);
+                                continue;
+                            }
+                            float x[32];
+                            tmem_ld32(from, x);
+                            float f = p.scale;
+                            if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
+                            else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
+                            tmem_wait_ld();
+                            if (d > 0 && c1 + 32 <= cols) {
+                                const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
+                                const float2 f2 = make_float2(f, f);
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 v = w4[i / 4];
+                                    const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(v.x, v.y));
+                                    const float2 hi2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(v.z, v.w));
+                                    pk[i / 2] = pack_bf16x2(lo2.x, lo2.y);
+                                    pk[i / 2 + 1] = pack_bf16x2(hi2.x, hi2.y);
+                                }
+                            } else {
+                                // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
+                                const float *v = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
+                                const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] * f * v[i] : 0.f;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                            }
+                            tmem_st16(to, pk);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[TileBars::WEIGHTS + (k & 1)]);
+                    }
+            }
+        };
+        run();
+    } else {
+        // ===================== scaling of the entering state's part, read-out =====================
+        const int quarter = warp & 3, half = (warp - 4 - kMath) >> 2, r = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const bool storer = warp == 4 + kMath;      // its first lane issues the stores
+        constexpr int CH = NZ / 2;
+        const auto run = [&]() {
+            int i = 0;
+            for (int it = 0; tile_item<NZ>(p, it, items, ttiles, ztiles, zgroup, w); ++it) {
+                if (!w.some) continue;
+                if (!w.live) {      // behind the sequence: zeros
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)w.bh * p.T + w.t0) * p.dz;
+                    const int c0 = w.z * NZ, width = (min(w.z_end * NZ, p.dz) - c0) / 8;
+                    for (int q = tid - 32 * (4 + kMath); q < 128 * width; q += 32 * kMath) {
+                        const int row = q / width, c = c0 + q % width * 8;
+                        if (w.t0 + row < p.T) *reinterpret_cast<uint4 *>(o + (size_t)row * p.dz + c) = make_uint4(0, 0, 0, 0);
+                    }
                     continue;
                 }
-                float x[32];
-                tmem_ld32(from, x);
-                float f = p.scale;
-                if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
-                else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
-                tmem_wait_ld();
-                if (d > 0 && c1 + 32 <= cols) {
-                    const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
-                    const float2 f2 = make_float2(f, f);
+                const float ld = head_log_decay(p.log_decay, w.bh % p.H);
+                const int t = w.t0 + r;
+                const float rho = p.rev ? decay_pow(ld, max(w.e - 1 - t, 0)) : p.scale * decay_pow(ld, t - w.s0 + 1);
+                for (int z = w.z; z < w.z_end; ++z, ++i) {
+                    const uint32_t acc = acc_at(i) + lanes + half * CH;
+                    if (!waitw(sh, &bar[TileBars::ENTRY + (i & 1)], (i >> 1) & 1, kWhereTileEntry)) return;
+                    if (w.entry) {
+                        tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 w = w4[i / 4];
-                        const float2 a = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(w.x, w.y));
-                        const float2 e2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(w.z, w.w));
-                        pk[i / 2] = pack_bf16x2(a.x, a.y);
-                        pk[i / 2 + 1] = pack_bf16x2(e2.x, e2.y);
+                        for (int c0 = 0; c0 < CH; c0 += 32) {
+                            float x[32];
+                            tmem_ld32(acc + c0, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) x[q] *= rho;
+                            tmem_st32(acc + c0, x);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
                     }
-                } else {
-                    // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
-                    const float *w = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
-                    const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[TileBars::SCALED + (i & 1)]);
+                    if (!waitw(sh, &bar[TileBars::DONE + (i & 1)], (i >> 1) & 1, kWhereTileDone)) return;
+                    tc_fence_after();
+                    // the staging memory is free once the store before has read it
+                    if (storer && lane == 0) {
+                        if (i > 0) tma_store_wait();
+                        mbar_arrive(&bar[TileBars::OUT_FREE]);
+                    }
+                    if (!waitw(sh, &bar[TileBars::OUT_FREE], i & 1, kWhereTileOut)) return;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] * f * w[i] : 0.f;
+                    for (int c0 = 0; c0 < CH; c0 += 32) {
+                        float x[32];
+                        tmem_ld32(acc + c0, x);
+                        tmem_wait_ld();
+                        const int col = half * CH + c0;
+                        uint8_t *box = out + (col / 64) * kUnit;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                }
-                tmem_st16(to, pk);
-            }
-            if (j == 0 && entry) {
-                if (!waitw(sh, &bar[TileBars::ENTRY], 0, kWhereTileEntry)) {
-                    alive = false;
-                    break;
-                }
-                tc_fence_after();
-                const float rho = p.rev ? decay_pow(ld, max(e - 1 - t, 0)) : p.scale * decay_pow(ld, t - s0 + 1);
-#pragma unroll
-                for (int c0 = 0; c0 < NZ / 2; c0 += 32) {
-                    float x[32];
-                    tmem_ld32(tm + lanes + half * (NZ / 2) + c0, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= rho;
-                    tmem_st32(tm + lanes + half * (NZ / 2) + c0, x);
-                }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[TileBars::WEIGHTS]);
-        }
-        alive = alive && waitw(sh, &bar[TileBars::DONE], 0, kWhereTileDone) && !*sh.abort_flag;
-        const bool ok = __all_sync(0xffffffffu, alive);
-        // every load and product is done: the ring's first units stage the output for the TMA store
-        if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int c0 = 0; c0 < NZ / 2; c0 += 32) {
-                float x[32];
-                tmem_ld32(tm + lanes + half * (NZ / 2) + c0, x);
-                tmem_wait_ld();
-                const int col = half * (NZ / 2) + c0;
-                uint8_t *box = ring + (col / 64) * kUnit;
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint4 v = make_uint4(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]),
-                                         pack_bf16x2(x[i + 4], x[i + 5]), pack_bf16x2(x[i + 6], x[i + 7]));
-                    if (t >= len) v = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(box + sw128_offset(r, (col % 64 + i) / 8)) = v;
+                        for (int q = 0; q < 32; q += 8) {
+                            uint4 v = make_uint4(pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3]),
+                                                 pack_bf16x2(x[q + 4], x[q + 5]), pack_bf16x2(x[q + 6], x[q + 7]));
+                            if (t >= w.len) v = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(box + sw128_offset(r, (col % 64 + q) / 8)) = v;
+                        }
+                    }
+                    tc_fence_before();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar[TileBars::TAKEN + (i & 1)]);
+                        mbar_arrive(&bar[TileBars::OUT_FULL]);
+                    }
+                    if (storer) {
+                        if (!waitw(sh, &bar[TileBars::OUT_FULL], i & 1, kWhereTileOut)) return;
+                        if (lane == 0) {
+                            for (int b = 0; b < NZ / 64; ++b)
+                                if (z * NZ + 64 * b < p.dz) tma_store_3d(&tmo, out + b * kUnit, z * NZ + 64 * b, w.t0, w.bh);
+                            tma_store_commit();
+                        }
+                    }
                 }
             }
-            tc_fence_before();
-            fence_proxy_async_smem();
-        }
-        named_barrier(1, 32 * kMath);
-        if (tid == 64 && ok) {
-            for (int b = 0; b < NZ / 64; ++b)
-                if (z0 + 64 * b < p.dz) tma_store_3d(&tmo, ring + b * kUnit, z0 + 64 * b, t0, bh);
-            tma_store_commit();
-            tma_store_wait();
-        }
+        };
+        run();
+        if (storer && lane == 0) tma_store_wait();
     }
     __syncthreads();
     __syncwarp();
-    if (warp == 1) tmem_dealloc(tm, 256);
+    if (warp == 1) tmem_dealloc(tm, 512);
 }
 
 // ---- launches -----------------------------------------------------------------------------------------------
@@ -743,21 +901,24 @@ template <int NZ>
 cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     const uint64_t BH = (uint64_t)p.B * p.H;
     const int nkx = (p.dx + 63) / 64, tt = (p.T + 127) / 128, zt = (p.dz + NZ - 1) / NZ;
-    // two blocks per SM where the block's own rows leave room for three units
-    const int room = nkx <= 4 ? 7 : 14, stages = room - nkx < kMaxStages ? room - nkx : kMaxStages;
+    // 224 KB: X twice where that leaves four slots for the ring, NZ / 64 boxes for the output, slots of two boxes
+    const int slot_units = nkx > 1 || NZ > 64 ? 2 : 1, nx = nkx <= 2 ? 2 : 1;
+    const int room = (14 - nx * nkx - NZ / 64) / slot_units, stages = room < kMaxRing ? room : kMaxRing;
+    // an item holds all z tiles of its tokens (X is read once) unless that leaves SMs without one
+    const int sms = sm_count(), zgroup = BH * tt >= 2ull * sms ? zt : 1;
+    const int items = (int)(BH * tt * ((zt + zgroup - 1) / zgroup)), grid = items < sms ? items : sms;
     CUtensorMap tmx, tmy, tmz, tms, tmo;
-    constexpr int R = NZ == 128 ? 64 : 128;
     const bool ok =
         make_tmap_3d_bf16(&tmx, p.x, p.dx, p.T, BH, 64, 128) && make_tmap_3d_bf16(&tmy, p.y, p.dx, p.T, BH, 64, 128) &&
-        make_tmap_3d_bf16(&tmz, p.z, p.dz, p.T, BH, 64, R) && make_tmap_3d_bf16(&tmo, p.out, p.dz, p.T, BH, 64, 128) &&
+        make_tmap_3d_bf16(&tmz, p.z, p.dz, p.T, BH, 64, 128) && make_tmap_3d_bf16(&tmo, p.out, p.dz, p.T, BH, 64, 128) &&
         (p.state_t ? make_tmap_3d_bf16(&tms, p.states, p.dz, p.dx, BH * p.nseg, 64, 64)
                    : make_tmap_3d_bf16(&tms, p.states, p.dx, p.dz, BH * p.nseg, 64, NZ));
     if (!ok) return cudaErrorInvalidValue;
-    const int smem = (nkx + stages) * kUnit + kTileTail;
+    const int smem = (nx * nkx + stages * slot_units + NZ / 64) * kUnit + kTileTail;
     cudaError_t e = cudaFuncSetAttribute(tile_tc_kernel<NZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tile_tc_kernel<NZ><<<(unsigned)(BH * tt * zt), kThreads, smem, s>>>(tmx, tmy, tmz, tms, tmo, p, tt, zt, nkx, stages,
-                                                                        status);
+    tile_tc_kernel<NZ><<<grid, kTileThreads, smem, s>>>(tmx, tmy, tmz, tms, tmo, p, items, tt, zt, zgroup, nkx, nx, stages,
+                                                        slot_units * kUnit, status);
     return cudaGetLastError();
 }
 
