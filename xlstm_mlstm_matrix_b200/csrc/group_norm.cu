@@ -14,6 +14,7 @@
 
 #include "arg_checks.cuh"
 #include "common.cuh"
+#include "fast_div.cuh"
 #include "../../include/xlstm_layer.h"
 
 namespace xlstm {
@@ -24,7 +25,7 @@ constexpr int kV = 8, kP = kV / 2;   // channels of one access per lane, and pai
 
 struct GroupNormP {
     int B, T, G, D, heads_major, act, tokens, tokens_per_block;
-    uint32_t t_mul, t_shift;    // division by T
+    FastDiv by_T;
     float eps, inv_D;
     const void *x;
     const float *weight, *bias;
@@ -131,13 +132,10 @@ __device__ __forceinline__ void act_both(int act, float2 x, float2 &f, float2 &d
     }
 }
 
-// n / d for 0 <= n < 2^31: the quotient by a product with ceil-like 2^(32+shift) / d.
-__device__ __forceinline__ int quotient(int n, uint32_t mul, uint32_t shift) {
-    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
-}
 __device__ __forceinline__ size_t x_offset(const GroupNormP &p, int token, int g) {
     if (!p.heads_major) return ((size_t)token * p.G + g) * p.D;
-    const int b = quotient(token, p.t_mul, p.t_shift), t = token - b * p.T;
+    int t = token;
+    const int b = split(t, p.by_T);
     return (((size_t)b * p.G + g) * p.T + t) * p.D;
 }
 
@@ -476,8 +474,7 @@ GroupNormP pack(const xlstm_group_norm_desc_t *d, long long blocks) {
     p.act = d->act; p.eps = d->eps; p.tokens = d->B * d->T;
     p.tokens_per_block = tokens_per_block(p.tokens, d->G, d->D, blocks);
     p.inv_D = 1.f / (float)d->D;
-    while ((1ull << p.t_shift) < (unsigned)d->T) ++p.t_shift;
-    p.t_mul = (uint32_t)(((1ull << 32) * ((1ull << p.t_shift) - (unsigned)d->T)) / (unsigned)d->T + 1);
+    p.by_T = fast_div((uint32_t)d->T);
     return p;
 }
 

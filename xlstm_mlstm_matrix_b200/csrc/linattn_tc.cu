@@ -19,14 +19,26 @@ namespace {
 
 // Codes of the bounded waits in the status block.
 enum : int {
-    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206, kWhereSumOut = 207,
+    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206, kWhereSumOut = 207, kWhereSumRaw = 208,
     kWhereTileEmpty = 211, kWhereTileX = 212, kWhereTileFull = 213, kWhereTileScores = 214, kWhereTileWeights = 215,
     kWhereTileEntry = 216, kWhereTileProduct = 217, kWhereTileDone = 218, kWhereTileTaken = 219, kWhereTileTable = 220,
-    kWhereTileOut = 221,
+    kWhereTileOut = 221, kWhereTileRaw = 222,
 };
 
 constexpr int kMath = 8;            // warps of one arithmetic role
 constexpr int kUnit = 16384;        // bytes of one ring unit
+
+// Where a role stands in the ring: the slot, and the parity of its current pass.
+struct RingAt {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // ---- entering states -----------------------------------------------------------------------------------
 // SEQ: a block carries one 128 x NX tile of a head's state through all segments and stores it at each segment's
@@ -52,7 +64,8 @@ struct StateCfg {
     static constexpr int OUT = 128 * NX * (SEQ ? 2 : 4);        // what a store leaves from
     static constexpr int OFF_BAR = OFF_OUT + OUT;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_SCALED = 2 * STAGES, B_ACC = 3 * STAGES, B_TAKEN = B_ACC + 2,
-                         B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_LAST = B_OUT_FREE + 1;
+                         B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_RAW = B_OUT_FREE + 1,
+                         B_LAST = B_RAW + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * (B_LAST + 1);
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int STATE = NX;                            // state's first column (IN_TMEM)
@@ -111,6 +124,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
         mbar_init(&bar[C::B_OUT_FULL], 8);
         mbar_init(&bar[C::B_OUT_FREE], 1);
+        mbar_init(&bar[C::B_RAW], 1);
         mbar_init(&bar[C::B_LAST], 1);
         *sh.abort_flag = 0;
         fence_mbar_init();
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     if (warp < 4) {
         if (warp == 0) {
             // ===================== loads =====================
-            int c = 0;          // stages issued
+            int c = 0, raw = 0;      // stages issued, those that a sequence ends in
             bool go = true;
             for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
                 const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
@@ -140,24 +154,24 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                             break;
                         }
                         uint8_t *Zs = sm + st * C::STAGE, *Ys = Zs + kPart;
-                        if (p.lens && t + kStep > w.len) {
-                            for (int b = 0; b < 2; ++b)
-                                load_box_rows<kStep>(Zs + 4096 * b,
-                                                     static_cast<const __nv_bfloat16 *>(p.z) + ((size_t)w.bh * p.T + t) * p.dv,
-                                                     p.dv, w.len - t, w.z0 + 64 * b, lane);
-                            for (int b = 0; b < NX / 64; ++b)
-                                load_box_rows<kStep>(Ys + 4096 * b,
-                                                     static_cast<const __nv_bfloat16 *>(p.y) + ((size_t)w.bh * p.T + t) * p.dqk,
-                                                     p.dqk, w.len - t, w.y0 + 64 * b, lane);
+                        // the stage the sequence ends in: rows behind its end become zeros before anyone sees it
+                        const bool ends = p.lens && t + kStep > w.len;
+                        uint64_t *landed = &bar[ends ? C::B_RAW : C::B_FULL + st];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(landed, kPart + C::Y_BYTES);
+                            for (int b = 0; b < 2; ++b) tma_load_3d(Zs + 4096 * b, &tmz, landed, w.z0 + 64 * b, t, w.bh);
+                            for (int b = 0; b < NX / 64; ++b) tma_load_3d(Ys + 4096 * b, &tmy, landed, w.y0 + 64 * b, t, w.bh);
+                        }
+                        if (ends) {
+                            if (!waitw(sh, landed, raw & 1, kWhereSumRaw)) {
+                                go = false;
+                                break;
+                            }
+                            ++raw;
+                            for (int b = 0; b < 2 + NX / 64; ++b) zero_rows<kStep>(Zs + 4096 * b, w.len - t, lane);
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar[C::B_FULL + st]);
-                        } else if (lane == 0) {
-                            mbar_arrive_expect_tx(&bar[C::B_FULL + st], kPart + C::Y_BYTES);
-                            for (int b = 0; b < 2; ++b)
-                                tma_load_3d(Zs + 4096 * b, &tmz, &bar[C::B_FULL + st], w.z0 + 64 * b, t, w.bh);
-                            for (int b = 0; b < NX / 64; ++b)
-                                tma_load_3d(Ys + 4096 * b, &tmy, &bar[C::B_FULL + st], w.y0 + 64 * b, t, w.bh);
                         }
                         __syncwarp();
                     }
@@ -167,42 +181,48 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (lane == 0)
                 for (int st = 0; st < C::STAGES; ++st)
                     if (c > st) drain_wait(&bar[C::B_FULL + st], ((c - 1 - st) / C::STAGES) & 1);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ===================== products =====================
+            // The whole warp walks the work, so that descriptors stay uniform; one lane issues.
             constexpr uint32_t id_u = make_idesc(128, NX, kFmtBF16, kFmtBF16, 1, 1);
-            int c = 0, g = 0;   // stages consumed, segments summed
-            bool go = true;
-            for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
-                const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
-                for (int k = 0; go && k < w.nm; ++k, ++g) {
-                    const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
-                    const uint32_t acc = tm + g % C::ACCS * NX;
-                    if (g >= C::ACCS && !wait1(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken)) {
-                        go = false;
-                        break;
-                    }
-                    for (int t = s0; t < e; t += kStep, ++c) {
-                        const int st = c % C::STAGES;
-                        if (!wait1(sh, &bar[C::B_SCALED + st], (c / C::STAGES) & 1, kWhereSumScaled)) {
-                            go = false;
-                            break;
+            const bool leader = elect_one();
+            const auto run = [&]() {
+                RingAt at, part;
+                int g = 0;          // segments summed
+                for (int item = blockIdx.x; item < items; item += gridDim.x) {
+                    const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
+                    for (int k = 0; k < w.nm; ++k, ++g) {
+                        const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
+                        const uint32_t acc = tm + g % C::ACCS * NX;
+                        if (g >= C::ACCS && !waitw(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken))
+                            return;
+                        for (int t = s0; t < e; t += kStep) {
+                            if (!waitw(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
+                            tc_fence_after();
+                            const uint64_t z = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
+                            const uint64_t y = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE + kPart), 4096, 1024);
+                            if (leader) {
+#pragma unroll
+                                for (int ks = 0; ks < kStep / 16; ++ks)
+#pragma unroll
+                                    for (int q = 0; q < 3; ++q)
+                                        mma_f16_ss(acc, z + (uint32_t)((q * kPart + ks * 2048) >> 4),
+                                                   y + (uint32_t)(ks * 2048 >> 4), id_u, t > s0 || ks > 0 || q > 0);
+                                tc_commit(&bar[C::B_EMPTY + at.slot]);
+                            }
+                            at.next(C::STAGES);
+                            part.next(C::PARTS);
                         }
-                        tc_fence_after();
-                        const uint64_t z = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + c % C::PARTS * C::PARTS_BYTES), 4096, 1024);
-                        const uint64_t y = smem_desc_sw128(smem_u32(sm + st * C::STAGE + kPart), 4096, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < kStep / 16; ++ks)
-#pragma unroll
-                            for (int part = 0; part < 3; ++part)
-                                mma_f16_ss(acc, z + (uint32_t)((part * kPart + ks * 2048) >> 4), y + (uint32_t)(ks * 2048 >> 4),
-                                           id_u, t > s0 || ks > 0 || part > 0);
-                        tc_commit(&bar[C::B_EMPTY + st]);
+                        if (leader) tc_commit(&bar[C::B_ACC + g % C::ACCS]);
                     }
-                    if (go) tc_commit(&bar[C::B_ACC + g % C::ACCS]);
                 }
+            };
+            run();
+            __syncwarp();
+            if (leader) {
+                tc_commit(&bar[C::B_LAST]);     // nothing in flight when tensor memory is freed
+                drain_wait(&bar[C::B_LAST], 0);
             }
-            tc_commit(&bar[C::B_LAST]);     // nothing in flight when tensor memory is freed
-            drain_wait(&bar[C::B_LAST], 0);
         }
     } else if (warp < 12) {
         // ===================== weights =====================
@@ -416,59 +436,66 @@ constexpr int kTileThreads = 640;       // TMA, two of products, one idle; eight
 constexpr int kMaxRing = 10;
 struct TileBars {                       // indices into the barrier array; pairs are one per buffer
     static constexpr int XFULL = 0, XFREE = 2, SCORES = 4, WEIGHTS = 6, PRODUCT = 8, ENTRY = 10, SCALED = 12, DONE = 14,
-                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, ZREADY = 23, RING = 25;
+                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, ZREADY = 23, RAW = 25, RING = 26;
 };
 constexpr int kTileTail = 2 * kTab * 4 + (TileBars::RING + 2 * kMaxRing) * 8 + 16;
 
 // What a block has to know of one item: 128 tokens of a head, with the z tiles z .. z_end of its output.
 struct TileItem {
     int bh, t0, len, n, s0, e, nj, z, z_end;
-    bool entry, some, live;      // some: an item at all; live: with tokens
+    float ld;                          // the head's log decay
+    bool entry, live, more;      // live: with tokens; more: there is an item
 };
-// The k-th item of this block: rounds over the grid, turned by 37 blocks each so that a block meets every place
-// within the segments (whose tiles have between one and G / 128 units).
-template <int NZ>
-__device__ __forceinline__ bool tile_item(const LinTileP &p, int k, int items, int ttiles, int ztiles, int zgroup, TileItem &w) {
-    int id = k * gridDim.x + (blockIdx.x + 37u * k) % gridDim.x;
-    w.some = w.live = false;
-    if (id >= items) return k * (int)gridDim.x < items;     // the last round's idle blocks
-    const int zgroups = (ztiles + zgroup - 1) / zgroup;
-    w.z = id % zgroups * zgroup;
-    w.z_end = min(w.z + zgroup, ztiles);
-    id /= zgroups;
-    w.t0 = id % ttiles * 128;
-    w.bh = id / ttiles;
-    w.len = seq_len(p.lens, w.bh / p.H, p.T);
-    w.n = w.t0 / p.G;
-    w.s0 = w.n * p.G;
-    w.e = min(w.s0 + p.G, w.len);
-    w.entry = p.rev ? (w.e < w.len || p.has_init) : (w.n > 0 || p.has_init);
-    // 128-token score tiles on this tile's past (future) side, its own first
-    w.nj = p.rev ? (w.e - w.t0 + 127) / 128 : (w.t0 - w.s0) / 128 + 1;
-    w.some = true;
-    w.live = w.t0 < w.len;
-    return true;
-}
-
-// Where a role stands in the ring: the slot, and the parity of its current pass.
-struct RingAt {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int stages) {
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
+// The items of a block: rounds over the grid, turned by 37 blocks each so that a block meets every place within the
+// segments (whose tiles have between one and G / 128 units).
+struct TilePlan {
+    int items, zgroup, ztiles, nkx, nx, stages, slot_bytes, seg_shift;     // segments of 2^seg_shift tokens
+    FastDiv by_zgroups, by_ttiles, by_H;
+};
+struct TileWalk {
+    int round, turn;
+    __device__ __forceinline__ TileWalk() : round(0), turn(blockIdx.x) {}
+};
+// The next item of the walk.  Not inlined: in every role's loop it would take a fifth of the kernel's code, and
+// instruction fetch is what the warps of this kernel wait for most.
+__device__ __noinline__ TileItem next_item(const LinTileP &p, const TilePlan &pl, TileWalk &walk) {
+    TileItem w;
+    w.live = false;
+    for (;;) {
+        int id = walk.round + walk.turn;
+        w.more = walk.round < pl.items;
+        if (!w.more) return w;
+        walk.round += gridDim.x;
+        walk.turn += 37;
+        while (walk.turn >= (int)gridDim.x) walk.turn -= gridDim.x;
+        if (id >= pl.items) continue;     // the last round's idle blocks
+        int zg = id, t = quotient(id, pl.by_zgroups);
+        zg -= t * (int)pl.by_zgroups.d;
+        w.bh = split(t, pl.by_ttiles);
+        w.z = zg * pl.zgroup;
+        w.z_end = min(w.z + pl.zgroup, pl.ztiles);
+        w.t0 = t * 128;
+        const int b = quotient(w.bh, pl.by_H);
+        w.len = seq_len(p.lens, b, p.T);
+        w.n = w.t0 >> pl.seg_shift;
+        w.s0 = w.n << pl.seg_shift;
+        w.e = min(w.s0 + p.G, w.len);
+        w.entry = p.rev ? (w.e < w.len || p.has_init) : (w.n > 0 || p.has_init);
+        // 128-token score tiles on this tile's past (future) side, its own first
+        w.nj = p.rev ? (w.e - w.t0 + 127) / 128 : (w.t0 - w.s0) / 128 + 1;
+        w.ld = head_log_decay(p.log_decay, w.bh - b * p.H);
+        w.live = w.t0 < w.len;
+        return w;
     }
-};
+}
 
 template <int NZ>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_tc_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmy,
                    const __grid_constant__ CUtensorMap tmz, const __grid_constant__ CUtensorMap tms,
-                   const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinTileP p, const int items,
-                   const int ttiles, const int ztiles, const int zgroup, const int nkx, const int nx, const int stages,
-                   const int slot_bytes, int32_t *status) {
+                   const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinTileP p,
+                   const __grid_constant__ TilePlan pl, int32_t *status) {
+    const int nkx = pl.nkx, nx = pl.nx, stages = pl.stages, slot_bytes = pl.slot_bytes;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *ring = sm + nx * nkx * kUnit, *out = ring + stages * slot_bytes;
     float *tabs = reinterpret_cast<float *>(out + NZ * 256) + 32;
@@ -497,6 +524,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(&bar[TileBars::OUT_FREE], 1);
         mbar_init(&bar[TileBars::LAST], 1);
         mbar_init(&bar[TileBars::LAST + 1], 1);
+        mbar_init(&bar[TileBars::RAW], 1);
         for (int i = 0; i < stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -518,7 +546,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     if (warp == 0) {
         // ===================== loads =====================
-        int u = 0, xi = 0;      // ring slots and items' X issued
+        int u = 0, xi = 0, raw = 0;      // ring slots and items' X issued; tiles that a sequence ends in
         const auto run = [&]() {
             RingAt at;
             const auto next = [&](int &st) {
@@ -527,7 +555,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 at.next(stages);
                 return ok;
             };
-            for (int k = 0; tile_item<NZ>(p, k, items, ttiles, ztiles, zgroup, w); ++k) {
+            TileWalk walk;
+            while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) continue;
                 const int xb = xi % nx;
                 if (xi >= nx && !waitw(sh, &bar[TileBars::XFREE + xb], (xi / nx - 1) & 1, kWhereTileX)) return;
@@ -568,19 +597,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             }
                         }
                         if (!next(st)) return;
-                        if (p.lens && t + 128 > w.len) {
-                            // the tile the sequence ends in: rows behind its end read as zeros, whatever is there
+                        // the tile the sequence ends in: rows behind its end become zeros before anyone sees it
+                        const bool ends = p.lens && t + 128 > w.len;
+                        uint64_t *landed = ends ? &bar[TileBars::RAW] : &full[st];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(landed, NZ / 64 * kUnit);
                             for (int b = 0; b < NZ / 64; ++b)
-                                load_box_rows<128>(ring + st * slot_bytes + b * kUnit,
-                                                   static_cast<const __nv_bfloat16 *>(p.z) + ((size_t)w.bh * p.T + t) * p.dz,
-                                                   p.dz, w.len - t, z * NZ + 64 * b, lane);
+                                tma_load_3d(ring + st * slot_bytes + b * kUnit, &tmz, landed, z * NZ + 64 * b, t, w.bh);
+                        }
+                        if (ends) {
+                            if (!waitw(sh, landed, raw & 1, kWhereTileRaw)) return;
+                            ++raw;
+                            for (int b = 0; b < NZ / 64; ++b) zero_rows<128>(ring + st * slot_bytes + b * kUnit, w.len - t, lane);
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&full[st]);
-                        } else if (lane == 0) {
-                            mbar_arrive_expect_tx(&full[st], NZ / 64 * kUnit);
-                            for (int b = 0; b < NZ / 64; ++b)
-                                tma_load_3d(ring + st * slot_bytes + b * kUnit, &tmz, &full[st], z * NZ + 64 * b, t, w.bh);
                         }
                         __syncwarp();
                         ++u;
@@ -605,7 +636,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto run = [&]() {
             RingAt at;
             int xi = 0, k = 0, i = 0;           // items, units and tiles so far
-            for (int r = 0; tile_item<NZ>(p, r, items, ttiles, ztiles, zgroup, w); ++r) {
+            TileWalk walk;
+            while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) continue;
                 const int xb = nx == 2 ? xi & 1 : 0;
                 if (!waitw(sh, &bar[TileBars::XFULL + xb], (nx == 2 ? xi >> 1 : xi) & 1, kWhereTileX)) return;
@@ -679,7 +711,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto run = [&]() {
             RingAt at;
             int k = 0, i = 0;
-            for (int r = 0; tile_item<NZ>(p, r, items, ttiles, ztiles, zgroup, w); ++r) {
+            TileWalk walk;
+            while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) continue;
                 for (int z = w.z; z < w.z_end; ++z, ++i)
                     for (int j = 0; j < w.nj; ++j, ++k) {
@@ -718,9 +751,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const auto run = [&]() {
             int k = 0, xi = 0;
-            for (int it = 0; tile_item<NZ>(p, it, items, ttiles, ztiles, zgroup, w); ++it) {
+            TileWalk walk;
+            while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) continue;
-                const float ld = head_log_decay(p.log_decay, w.bh % p.H);
+                const float ld = w.ld;
                 // Column c of a score tile at distance d tiles carries l^(128 (d - 1)) times tab[c] times the row's power.
                 // A warp that writes this item's table has seen all warps write the one before, and so leave the one
                 // before that, whose place this is.
@@ -751,31 +785,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 tmem_st16(to, pk);
                                 continue;
                             }
-                            float x[32];
-                            tmem_ld32(from, x);
                             float f = p.scale;
                             if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
                             else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
-                            tmem_wait_ld();
-                            if (d > 0 && c1 + 32 <= cols) {
-                                const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
-                                const float2 f2 = make_float2(f, f);
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 v = w4[i / 4];
-                                    const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(v.x, v.y));
-                                    const float2 hi2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(v.z, v.w));
-                                    pk[i / 2] = pack_bf16x2(lo2.x, lo2.y);
-                                    pk[i / 2 + 1] = pack_bf16x2(hi2.x, hi2.y);
-                                }
-                            } else {
+                            if (d == 0 || c1 + 32 > cols) {
                                 // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
                                 const float *v = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
                                 const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
+#pragma unroll 1
+                                for (int g = 0; g < 32; g += 8) {
+                                    float x[8];
+                                    tmem_ld8(from + g, x);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] * f * v[i] : 0.f;
+                                    for (int i = 0; i < 8; ++i) x[i] = g + i >= lo && g + i < hi ? x[i] * f * v[g + i] : 0.f;
+                                    tmem_st4(to + g / 2, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                             pack_bf16x2(x[6], x[7]));
+                                }
+                                continue;
+                            }
+                            float x[32];
+                            tmem_ld32(from, x);
+                            tmem_wait_ld();
+                            const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
+                            const float2 f2 = make_float2(f, f);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 v = w4[i / 4];
+                                const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(v.x, v.y));
+                                const float2 hi2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(v.z, v.w));
+                                pk[i / 2] = pack_bf16x2(lo2.x, lo2.y);
+                                pk[i / 2 + 1] = pack_bf16x2(hi2.x, hi2.y);
                             }
                             tmem_st16(to, pk);
                         }
@@ -795,8 +835,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         constexpr int CH = NZ / 2;
         const auto run = [&]() {
             int i = 0;
-            for (int it = 0; tile_item<NZ>(p, it, items, ttiles, ztiles, zgroup, w); ++it) {
-                if (!w.some) continue;
+            TileWalk walk;
+            while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) {      // behind the sequence: zeros
                     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)w.bh * p.T + w.t0) * p.dz;
                     const int c0 = w.z * NZ, width = (min(w.z_end * NZ, p.dz) - c0) / 8;
@@ -806,7 +846,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     continue;
                 }
-                const float ld = head_log_decay(p.log_decay, w.bh % p.H);
+                const float ld = w.ld;
                 const int t = w.t0 + r;
                 const float rho = p.rev ? decay_pow(ld, max(w.e - 1 - t, 0)) : p.scale * decay_pow(ld, t - w.s0 + 1);
                 for (int z = w.z; z < w.z_end; ++z, ++i) {
@@ -814,7 +854,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!waitw(sh, &bar[TileBars::ENTRY + (i & 1)], (i >> 1) & 1, kWhereTileEntry)) return;
                     if (w.entry) {
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c0 = 0; c0 < CH; c0 += 32) {
                             float x[32];
                             tmem_ld32(acc + c0, x);
@@ -836,7 +876,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         mbar_arrive(&bar[TileBars::OUT_FREE]);
                     }
                     if (!waitw(sh, &bar[TileBars::OUT_FREE], i & 1, kWhereTileOut)) return;
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < CH; c0 += 32) {
                         float x[32];
                         tmem_ld32(acc + c0, x);
@@ -917,8 +957,11 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     const int smem = (nx * nkx + stages * slot_units + NZ / 64) * kUnit + kTileTail;
     cudaError_t e = cudaFuncSetAttribute(tile_tc_kernel<NZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tile_tc_kernel<NZ><<<grid, kTileThreads, smem, s>>>(tmx, tmy, tmz, tms, tmo, p, items, tt, zt, zgroup, nkx, nx, stages,
-                                                        slot_units * kUnit, status);
+    int seg_shift = 7;
+    while ((1 << seg_shift) < p.G) ++seg_shift;
+    const TilePlan pl{items, zgroup, zt, nkx, nx, stages, slot_units * kUnit, seg_shift,
+                      fast_div((zt + zgroup - 1) / zgroup), fast_div(tt), fast_div(p.H)};
+    tile_tc_kernel<NZ><<<grid, kTileThreads, smem, s>>>(tmx, tmy, tmz, tms, tmo, p, pl, status);
     return cudaGetLastError();
 }
 

@@ -1,5 +1,6 @@
 // Device pieces of the tensor-core linear attention beside sm100.cuh and tc_common.cuh.
 #pragma once
+#include "fast_div.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"
 
@@ -48,6 +49,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // l^n and l^m as two floats each: (l^n high, rest, l^m high, rest).  One rounded factor, applied once per segment,
 // would drift the oldest tokens' weight by a thousand of its roundings.
 __device__ __noinline__ float4 decay_factors(float ld, int n, int m) {
@@ -55,27 +68,11 @@ __device__ __noinline__ float4 decay_factors(float ld, int n, int m) {
     return make_float4((float)a, (float)(a - (double)(float)a), (float)b, (float)(b - (double)(float)b));
 }
 
-// One warp brings R rows x 64 columns of a row-major bf16 matrix (ncols wide, from column col0) into a
-// swizzled box, zeros at and past row `rows` and past the last column: for the tile a sequence ends in,
-// where a TMA copy would bring what lies behind its end.
+// One warp zeroes rows first .. R - 1 of a swizzled box (rows are 128 contiguous bytes whatever the swizzle): for the tile
+// a sequence ends in, where the copy brought what lies behind its end.
 template <int R>
-__device__ __noinline__ void load_box_rows(uint8_t *box, const __nv_bfloat16 *src, int ncols, int rows, int col0,
-                                           int lane) {
-#pragma unroll 1
-    for (int e0 = 0; e0 < R * 8; e0 += 256) {   // R a multiple of 32
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + 32 * i + lane, r = e >> 3, col = col0 + 8 * (e & 7);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows && col < ncols) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * ncols + col));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + 32 * i + lane;
-            *reinterpret_cast<uint4 *>(box + sw128_offset(e >> 3, e & 7)) = v[i];
-        }
-    }
+__device__ __forceinline__ void zero_rows(uint8_t *box, int first, int lane) {
+    for (int o = max(first, 0) * 128 + lane * 16; o < R * 128; o += 512) *reinterpret_cast<uint4 *>(box + o) = make_uint4(0, 0, 0, 0);
 }
 
 // w times eight bf16 values as three bf16 parts: the top 8 significand bits of w v, the next 8 and the last 8.  Cut off
