@@ -75,19 +75,32 @@ constexpr int kStateThreads = 640;       // TMA, MMA, two idle warps; two groups
 constexpr int kFold = 384;               // first thread of the fold warps
 
 // One tile's walk over its segments, the same in every role.
+struct StatePlan {
+    int items;
+    FastDiv by_ytiles, by_ztiles, by_nseg, by_H;
+};
 struct StateWalk {
     int bh, z0, y0, len, nseg, nm;       // segments of the sequence, and those whose sum is formed
     int first;                           // SUM: the block's only segment
+    float ld;
 };
+// (Not inlined, for the kernel's code size; its divisions are products.)
 template <int NX, bool SEQ>
-__device__ __forceinline__ StateWalk state_walk(const LinStateP &p, int item, int ztiles, int ytiles) {
+__device__ __noinline__ StateWalk state_walk(const LinStateP &p, const StatePlan &pl, int item) {
     StateWalk w;
-    w.y0 = item % ytiles * NX; item /= ytiles;
-    w.z0 = item % ztiles * 128; item /= ztiles;
+    int rest = quotient(item, pl.by_ytiles);
+    w.y0 = (item - rest * (int)pl.by_ytiles.d) * NX;
+    w.bh = split(rest, pl.by_ztiles);
+    w.z0 = rest * 128;
     w.first = 0;
-    if (!SEQ) { w.first = item % p.nseg; item /= p.nseg; }
-    w.bh = item;
-    w.len = seq_len(p.lens, item / p.H, p.T);
+    if (!SEQ) {
+        int n = w.bh;
+        w.bh = split(n, pl.by_nseg);
+        w.first = n;
+    }
+    const int b = quotient(w.bh, pl.by_H);
+    w.ld = head_log_decay(p.log_decay, w.bh - b * p.H);
+    w.len = seq_len(p.lens, b, p.T);
     w.nseg = (w.len + p.G - 1) / p.G;
     // the sum of the chain's last segment only enters the final state
     if (SEQ) w.nm = p.last ? w.nseg : w.nseg - 1;
@@ -103,8 +116,8 @@ __device__ __forceinline__ int segment_of(const LinStateP &p, const StateWalk &w
 template <int NX, bool SEQ>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_tc_kernel(const __grid_constant__ CUtensorMap tmz, const __grid_constant__ CUtensorMap tmy,
-                    const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinStateP p, const int items,
-                    const int ztiles, const int ytiles, int32_t *status) {
+                    const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinStateP p,
+                    const __grid_constant__ StatePlan pl, int32_t *status) {
     using C = StateCfg<NX, SEQ>;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
@@ -143,8 +156,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             // ===================== loads =====================
             int c = 0, raw = 0;      // stages issued, those that a sequence ends in
             bool go = true;
-            for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
-                const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
+            for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
+                const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
                 for (int k = 0; go && k < w.nm; ++k) {
                     const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                     for (int t = s0; t < e; t += kStep, ++c) {
@@ -189,8 +202,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             const auto run = [&]() {
                 RingAt at, part;
                 int g = 0;          // segments summed
-                for (int item = blockIdx.x; item < items; item += gridDim.x) {
-                    const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
+                for (int item = blockIdx.x; item < pl.items; item += gridDim.x) {
+                    const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
                     for (int k = 0; k < w.nm; ++k, ++g) {
                         const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                         const uint32_t acc = tm + g % C::ACCS * NX;
@@ -230,9 +243,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int t128 = tid & 127, group = (warp - 4) >> 2;
         int c = 0;
         bool go = true;
-        for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
-            const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
-            const float ld = head_log_decay(p.log_decay, w.bh % p.H);
+        for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
+            const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
+            const float ld = w.ld;
             for (int k = 0; go && k < w.nm; ++k) {
                 const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                 for (int t = s0; t < e; t += kStep, ++c) {
@@ -308,11 +321,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             ++stores;
             return true;
         };
-        for (int item = blockIdx.x; go && item < items; item += gridDim.x) {
-            const StateWalk w = state_walk<NX, SEQ>(p, item, ztiles, ytiles);
+        for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
+            const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
             if (SEQ) {
-                const float ld = head_log_decay(p.log_decay, w.bh % p.H);
-                const float4 f = decay_factors(ld, p.G, w.len - (w.nseg - 1) * p.G);
+                // (nothing is scaled where the chain starts from zero and ends after its first segment)
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.init || w.nseg > 1) f = decay_factors(w.ld, p.G, w.len - (w.nseg - 1) * p.G);
                 const size_t own = ((size_t)w.bh * p.dv + w.z0 + r) * p.dqk + w.y0 + half * CH;   // this thread's columns
                 const bool row = w.z0 + r < p.dv;
                 const auto inside = [&](int i) { return row && w.y0 + half * CH + i < p.dqk; };
@@ -362,16 +376,24 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 32) {
                         float(&v)[32] = x[c0 / 32 % KEPT];
-                        if (C::IN_TMEM) tmem_ld32(own_tm + C::STATE + c0, v);
-#pragma unroll
-                        for (int c1 = 0; c1 < 32; c1 += 16) {
-                            float u[16];
-                            tmem_ld16(own_tm + g % C::ACCS * NX + c0 + c1, u);
+                        if (C::IN_TMEM) {       // both reads at once: the products wait for this loop
+                            float u[32];
+                            tmem_ld32(own_tm + C::STATE + c0, v);
+                            tmem_ld32(own_tm + c0, u);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[c1 + i] = fmaf(v[c1 + i], hi, fmaf(v[c1 + i], lo, u[i]));
+                            for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], hi, fmaf(v[i], lo, u[i]));
+                            tmem_st32(own_tm + C::STATE + c0, v);
+                        } else {
+#pragma unroll
+                            for (int c1 = 0; c1 < 32; c1 += 16) {
+                                float u[16];
+                                tmem_ld16(own_tm + g % C::ACCS * NX + c0 + c1, u);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[c1 + i] = fmaf(v[c1 + i], hi, fmaf(v[c1 + i], lo, u[i]));
+                            }
                         }
-                        if (C::IN_TMEM) tmem_st32(own_tm + C::STATE + c0, v);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -933,7 +955,8 @@ cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
     const int zt = (p.dv + 127) / 128, yt = (p.dqk + NX - 1) / NX;
     const size_t items = BH * zt * yt * (SEQ ? 1 : p.nseg);
     const unsigned grid = items < (size_t)sm_count() ? (unsigned)items : (unsigned)sm_count();
-    kernel<<<grid, kStateThreads, C::BYTES, s>>>(tmz, tmy, tmo, p, (int)items, zt, yt, status);
+    const StatePlan pl{(int)items, fast_div(yt), fast_div(zt), fast_div(p.nseg), fast_div(p.H)};
+    kernel<<<grid, kStateThreads, C::BYTES, s>>>(tmz, tmy, tmo, p, pl, status);
     return cudaGetLastError();
 }
 
