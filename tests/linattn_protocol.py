@@ -16,13 +16,13 @@ def _copy(P, bar: str, tag: int):
     P.arrive(f"copy {bar} {tag}", bar, tag)
 
 
-def tile_protocol(items, nslots: int, stages: int, nx: int, z_relay: bool = True) -> Protocol:
-    """tile_tc_kernel.  items: one list per item (128 tokens of a head) of its tiles, each (units, entry): how many score
-    units the tile has and whether a state enters; nslots: ring slots of Y (and of the state); nx: X buffers.
-    z_relay=False gives the earlier form, in which the warp of the scores skipped Z's slots."""
+def tile_protocol(items, nslots: int, stages: int, nx: int, relays: int = 4) -> Protocol:
+    """tile_tc_kernel.  items: per item (128 tokens of a head) how many tiles of output columns it has, how many score
+    units serve them, and whether a state enters; nslots: ring slots of Y (and of the state); nx: X buffers; relays: the
+    barriers that pass Z's arrivals on (0: the earlier form, in which the warp of the scores skipped Z's slots)."""
     P = Protocol()
-    u = k = i = 0
-    for xi, tiles in enumerate(items):
+    u = k0 = i = zc = 0
+    for xi, (nz, units, entry) in enumerate(items):
         xb = xi % nx
         if xi >= nx:
             P.wait("load", f"XFREE{xb}", xi - nx)
@@ -30,27 +30,32 @@ def tile_protocol(items, nslots: int, stages: int, nx: int, z_relay: bool = True
         P.wait("scores", f"XFULL{xb}", xi)
         P.arrive("weights", "TABLE", xi)
         P.wait("weights", "TABLE", xi)
-        for ti, (units, entry) in enumerate(tiles):
+        for j in range(units):
+            P.wait("weights", f"SCORES{(k0 + j) & 1}", k0 + j)
+            P.arrive("weights", f"WEIGHTS{(k0 + j) & 1}", k0 + j)
+        for z in range(nz):
             b = i & 1
             for j in range(units):
+                k = k0 + j
                 s = k & 1
-                slots_y = list(range(u, u + nslots))
-                u += nslots
+                slots_y = list(range(u, u + nslots)) if z == 0 else []
+                u += len(slots_y)
                 slots_e = list(range(u, u + nslots)) if j == 0 and entry else []
                 u += len(slots_e)
-                z = u
+                at = u
                 u += 1
-                for v in slots_y + slots_e + [z]:
+                for v in slots_y + slots_e + [at]:
                     if v >= stages:
                         P.wait("load", f"EMPTY{v % stages}", v - stages)
                     _copy(P, f"FULL{v % stages}", v)
                 # scores and the state's part
-                if k >= 2:
-                    P.wait("scores", f"PRODUCT{s}", k - 2)
-                for v in slots_y:
-                    P.wait("scores", f"FULL{v % stages}", v)
-                    P.arrive("scores", f"EMPTY{v % stages}", v)
-                P.arrive("scores", f"SCORES{s}", k)
+                if z == 0:
+                    if k >= 2:
+                        P.wait("scores", f"PRODUCT{s}", k - 2)
+                    for v in slots_y:
+                        P.wait("scores", f"FULL{v % stages}", v)
+                        P.arrive("scores", f"EMPTY{v % stages}", v)
+                    P.arrive("scores", f"SCORES{s}", k)
                 if j == 0:
                     if i >= 2:
                         P.wait("scores", f"TAKEN{b}", i - 2)
@@ -58,24 +63,23 @@ def tile_protocol(items, nslots: int, stages: int, nx: int, z_relay: bool = True
                         P.wait("scores", f"FULL{v % stages}", v)
                         P.arrive("scores", f"EMPTY{v % stages}", v)
                     P.arrive("scores", f"ENTRY{b}", i)
-                if j == units - 1 and ti == len(tiles) - 1:
+                if j == units - 1 and z == nz - 1:
                     P.arrive("scores", f"XFREE{xb}", xi)
-                if z_relay:
-                    P.wait("scores", f"FULL{z % stages}", z)
-                    P.arrive("scores", f"ZREADY{s}", k)
+                if relays:
+                    P.wait("scores", f"FULL{at % stages}", at)
+                    P.arrive("scores", f"ZREADY{zc % relays}", zc)
                 # weighted scores against Z
                 if j == 0:
                     P.wait("products", f"SCALED{b}", i)
-                if z_relay:
-                    P.wait("products", f"ZREADY{s}", k)
-                P.wait("products", f"FULL{z % stages}", z)
-                P.wait("products", f"WEIGHTS{s}", k)
-                P.arrive("products", f"EMPTY{z % stages}", z)
-                P.arrive("products", f"PRODUCT{s}", k)
-                # weights
-                P.wait("weights", f"SCORES{s}", k)
-                P.arrive("weights", f"WEIGHTS{s}", k)
-                k += 1
+                if relays:
+                    P.wait("products", f"ZREADY{zc % relays}", zc)
+                P.wait("products", f"FULL{at % stages}", at)
+                if z == 0:
+                    P.wait("products", f"WEIGHTS{s}", k)
+                P.arrive("products", f"EMPTY{at % stages}", at)
+                if z == nz - 1:
+                    P.arrive("products", f"PRODUCT{s}", k)
+                zc += 1
             P.arrive("products", f"DONE{b}", i)
             # scaling and read-out: the storer frees the staging memory and stores from it
             P.wait("read-out", f"ENTRY{b}", i)
@@ -87,6 +91,7 @@ def tile_protocol(items, nslots: int, stages: int, nx: int, z_relay: bool = True
             P.arrive("read-out", "OUT_FULL", i)
             P.wait("read-out", "OUT_FULL", i)
             i += 1
+        k0 += units
     return P
 
 

@@ -3,12 +3,14 @@ import pytest
 
 from linattn_protocol import state_protocol, tile_protocol
 
-ITEMS = {
-    "single": [[(1, False)]],
-    "one segment": [[(j + 1, True)] for j in range(2)] * 3,
-    "first segment, then others": [[(1, False)], [(2, False)], [(1, True)], [(2, True)], [(3, True)], [(4, True)]],
-    "several z tiles": [[(2, True)] * 4, [(1, True)] * 4, [(1, False)] * 3, [(4, False)] * 2],
-    "long": [[(1, True)]] * 9,
+ITEMS = {   # tiles of output columns, score units, a state enters
+    "single": [(1, 1, False)],
+    "one column tile": [(1, 1, False), (1, 2, False), (1, 1, True), (1, 2, True)] * 3,
+    "two": [(2, 2, True), (2, 1, True), (2, 1, False), (2, 2, False)] * 2,
+    "four": [(4, 2, True), (4, 1, True), (4, 1, False), (4, 2, False), (4, 2, True)],
+    "eight": [(8, 1, True), (8, 2, True), (8, 1, False)],
+    "long": [(1, 1, True)] * 9,
+    "ragged": [(4, 2, True), (4, 1, False), (1, 1, False), (1, 2, True), (3, 2, True)],
 }
 
 
@@ -20,8 +22,14 @@ def test_tile_kernel(items, nslots, stages, nx):
 
 def test_skipped_slots_are_rejected():
     """The earlier form: the warp of the scores skipped Z's slots, and could take the open phase of one for its next."""
-    found = [tile_protocol(items, 4, 2, 1, z_relay=False).check() for items in ITEMS.values()]
+    found = [tile_protocol(items, 4, 2, 1, relays=0).check() for items in ITEMS.values()]
     assert any(any("underrun" in p and "scores" in p for p in f) for f in found)
+
+
+def test_two_relays_are_too_few():
+    """Z's arrivals run up to four ahead of the products that use them."""
+    found = [tile_protocol(items, 1, 5, 2, relays=2).check() for items in ITEMS.values()]
+    assert any(any("overrun" in p and "ZREADY" in p for p in f) for f in found)
 
 
 @pytest.mark.parametrize("stages,parts,accs", [(4, 2, 1), (6, 3, 2), (6, 2, 2)])

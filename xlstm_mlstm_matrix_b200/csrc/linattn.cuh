@@ -91,7 +91,7 @@ __device__ __forceinline__ int job_of_block(const LinJobs<P, MOST> &jobs, unsign
 }
 
 // The launches behind both calls; grids stay below 2^31 blocks by the checks of the C ABI.
-constexpr int kSimtSegment = 64;                                              // the fp32 kernels' G
+constexpr int kSimtSegment = 64, kTcSegment = 256;                               // G of the fp32 and the bf16 kernels
 cudaError_t linattn_sums_simt(LinStates jobs, cudaStream_t s);                     // fp32
 cudaError_t linattn_tile_simt(LinTiles jobs, int32_t *status, cudaStream_t s);     // clears status
 // bf16: the states at once where linattn_states_seq, else the sums for linattn_chain

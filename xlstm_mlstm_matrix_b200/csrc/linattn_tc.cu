@@ -447,18 +447,20 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 }
 
 // ---- output tiles ---------------------------------------------------------------------------------------
-// One persistent block per SM.  Its work is a stream of units: 128 tokens x NZ columns of the output against 128 tokens
-// of the segment.  While eight warps weight the scores of unit k, the tensor core forms those of unit k + 1 (scores and
-// accumulators have two buffers each, all 512 columns), and eight more warps scale the entering state's part and read
-// finished tiles out.  Two warps issue the products, one the scores and the state's part, one the weighted scores
-// against Z: a wait and a commit per slot cost the issuing thread several hundred cycles, more than the eight products
-// of a slot take.
+// One persistent block per SM.  An item is 128 tokens of a head: their scores against the one or two 128-token tiles of the
+// segment on their past (future) side are formed and weighted once, into the two score buffers, and serve every tile of
+// NZ output columns.  While eight warps weight the scores of one unit the tensor core forms those of the next, the
+// accumulators have two buffers (512 columns with the scores), and eight more warps scale the entering state's part and
+// read finished tiles out.  Two warps issue the products, one the scores and the state's part, one the weighted scores
+// against Z; both walk the work as whole warps, so that operands stay in uniform registers (issued from a single-thread
+// branch a product took 110 to 170 cycles, not 64).
 constexpr int kTab = 32 + 132 + 32;     // powers of the decay, room for masked columns on both sides
 constexpr int kTileThreads = 640;       // TMA, two of products, one idle; eight warps of weights; eight of scaling and read-out
 constexpr int kMaxRing = 10;
 struct TileBars {                       // indices into the barrier array; pairs are one per buffer
     static constexpr int XFULL = 0, XFREE = 2, SCORES = 4, WEIGHTS = 6, PRODUCT = 8, ENTRY = 10, SCALED = 12, DONE = 14,
-                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, ZREADY = 23, RAW = 25, RING = 26;
+                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, RAW = 23, ZREADY = 24 /* four */,
+                         RING = 28;
 };
 constexpr int kTileTail = 2 * kTab * 4 + (TileBars::RING + 2 * kMaxRing) * 8 + 16;
 
@@ -533,6 +535,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&bar[TileBars::XFULL + i], 1);
             mbar_init(&bar[TileBars::XFREE + i], 1);
             mbar_init(&bar[TileBars::ZREADY + i], 1);
+            mbar_init(&bar[TileBars::ZREADY + 2 + i], 1);
             mbar_init(&bar[TileBars::SCORES + i], 1);
             mbar_init(&bar[TileBars::WEIGHTS + i], kMath);
             mbar_init(&bar[TileBars::PRODUCT + i], 1);
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int j = 0; j < w.nj; ++j) {
                         const int t = w.t0 + j * dir;
                         int st;
-                        for (int c = 0; c < nkx; c += 2, ++u) {
+                        for (int c = 0; z == w.z && c < nkx; c += 2, ++u) {
                             if (!next(st)) return;
                             if (lane == 0) {
                                 const int two = c + 1 < nkx;
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool leader = elect_one();
         const auto run = [&]() {
             RingAt at;
-            int xi = 0, k = 0, i = 0;           // items, units and tiles so far
+            int xi = 0, k = 0, i = 0, zc = 0;           // items, units, tiles and slots of Z so far
             TileWalk walk;
             while ((w = next_item(p, pl, walk)).more) {
                 if (!w.live) continue;
@@ -665,27 +668,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (!waitw(sh, &bar[TileBars::XFULL + xb], (nx == 2 ? xi >> 1 : xi) & 1, kWhereTileX)) return;
                 const uint64_t x = smem_desc_sw128(smem_u32(sm + xb * nkx * kUnit), 16, 1024);
                 for (int z = w.z; z < w.z_end; ++z, ++i)
-                    for (int j = 0; j < w.nj; ++j, ++k) {
-                        // the weighted scores of two units ago share the columns
-                        if (k >= 2 && !waitw(sh, &bar[TileBars::PRODUCT + (k & 1)], (k / 2 - 1) & 1, kWhereTileProduct)) return;
-                        tc_fence_after();
-                        const uint32_t sc = scores_at(k), acc = acc_at(i);
-                        for (int c = 0; c < nkx; c += 2) {
-                            if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
-                            const uint64_t y = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), 16, 1024);
-                            const uint64_t xc = x + (uint32_t)(c * kUnit >> 4);
-                            if (leader) {
+                    for (int j = 0; j < w.nj; ++j) {
+                        const uint32_t acc = acc_at(i);
+                        if (z == w.z) {
+                            // the weighted scores of two units ago share the columns
+                            if (k >= 2 && !waitw(sh, &bar[TileBars::PRODUCT + (k & 1)], (k / 2 - 1) & 1, kWhereTileProduct)) return;
+                            tc_fence_after();
+                            const uint32_t sc = scores_at(k);
+                            for (int c = 0; c < nkx; c += 2) {
+                                if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
+                                const uint64_t y = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), 16, 1024);
+                                const uint64_t xc = x + (uint32_t)(c * kUnit >> 4);
+                                if (leader) {
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks) mma_f16_ss(sc, xc + 2 * ks, y + 2 * ks, id_s, c > 0 || ks > 0);
-                                if (c + 1 < nkx)
+                                    for (int ks = 0; ks < 4; ++ks) mma_f16_ss(sc, xc + 2 * ks, y + 2 * ks, id_s, c > 0 || ks > 0);
+                                    if (c + 1 < nkx)
 #pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        mma_f16_ss(sc, xc + (kUnit >> 4) + 2 * ks, y + (kUnit >> 4) + 2 * ks, id_s, 1);
-                                tc_commit(&empty[at.slot]);
+                                        for (int ks = 0; ks < 4; ++ks)
+                                            mma_f16_ss(sc, xc + (kUnit >> 4) + 2 * ks, y + (kUnit >> 4) + 2 * ks, id_s, 1);
+                                    tc_commit(&empty[at.slot]);
+                                }
+                                at.next(stages);
                             }
-                            at.next(stages);
+                            if (leader) tc_commit(&bar[TileBars::SCORES + (k & 1)]);
+                            ++k;
                         }
-                        if (leader) tc_commit(&bar[TileBars::SCORES + (k & 1)]);
                         if (j == 0) {
                             // the tile that used the accumulator before has been read out
                             if (i >= 2 && !waitw(sh, &bar[TileBars::TAKEN + (i & 1)], (i / 2 - 1) & 1, kWhereTileTaken)) return;
@@ -714,7 +721,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         // that skipped a phase of a slot could take the one before it for the next one.
                         if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
                         at.next(stages);
-                        if (leader) mbar_arrive(&bar[TileBars::ZREADY + (k & 1)]);
+                        if (leader) mbar_arrive(&bar[TileBars::ZREADY + (zc & 3)]);
+                        ++zc;
                     }
                 ++xi;
             }
@@ -732,17 +740,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int nys = (nkx + 1) / 2;
         const auto run = [&]() {
             RingAt at;
-            int k = 0, i = 0;
+            int k0 = 0, i = 0, zc = 0;      // the item's first unit; tiles and slots of Z so far
             TileWalk walk;
-            while ((w = next_item(p, pl, walk)).more) {
+            for (; (w = next_item(p, pl, walk)).more; k0 += w.live ? w.nj : 0) {
                 if (!w.live) continue;
                 for (int z = w.z; z < w.z_end; ++z, ++i)
-                    for (int j = 0; j < w.nj; ++j, ++k) {
-                        for (int c = j == 0 && w.entry ? 2 * nys : nys; c > 0; --c) at.next(stages);     // Y's and the state's slots
+                    for (int j = 0; j < w.nj; ++j, ++zc) {
+                        const int k = k0 + j;
+                        // Y's and the state's slots
+                        for (int c = (z == w.z ? nys : 0) + (j == 0 && w.entry ? nys : 0); c > 0; --c) at.next(stages);
                         if (j == 0 && !waitw(sh, &bar[TileBars::SCALED + (i & 1)], (i >> 1) & 1, kWhereTileEntry)) return;
-                        if (!waitw(sh, &bar[TileBars::ZREADY + (k & 1)], (k >> 1) & 1, kWhereTileFull)) return;
+                        if (!waitw(sh, &bar[TileBars::ZREADY + (zc & 3)], (zc >> 2) & 1, kWhereTileFull)) return;
                         if (!waitw(sh, &full[at.slot], at.phase, kWhereTileFull)) return;
-                        if (!waitw(sh, &bar[TileBars::WEIGHTS + (k & 1)], (k >> 1) & 1, kWhereTileWeights)) return;
+                        if (z == w.z && !waitw(sh, &bar[TileBars::WEIGHTS + (k & 1)], (k >> 1) & 1, kWhereTileWeights)) return;
                         tc_fence_after();
                         const uint64_t zd = smem_desc_sw128(smem_u32(ring + at.slot * slot_bytes), kUnit, 1024);
                         const uint32_t acc = acc_at(i), ps = scores_at(k);
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 mma_f16_ts(acc, ps + 64 * (q / 4) + 8 * (q % 4), zd + (uint32_t)(q * 2048 >> 4), id_pz,
                                            w.entry || j > 0 || q > 0);
                             tc_commit(&empty[at.slot]);
-                            tc_commit(&bar[TileBars::PRODUCT + (k & 1)]);
+                            if (z == w.z_end - 1) tc_commit(&bar[TileBars::PRODUCT + (k & 1)]);
                             if (j == w.nj - 1) tc_commit(&bar[TileBars::DONE + (i & 1)]);
                         }
                         at.next(stages);
@@ -787,65 +797,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (lane == 0) mbar_arrive(&bar[TileBars::TABLE]);
                 if (!waitw(sh, &bar[TileBars::TABLE], xi & 1, kWhereTileTable)) return;
                 ++xi;
-                for (int z = w.z; z < w.z_end; ++z)
-                    for (int j = 0; j < w.nj; ++j, ++k) {
-                        const uint32_t tm_s = scores_at(k);
-                        const int cols = p.rev ? min(128, w.e - (w.t0 + 128 * j)) : 128;     // live columns
-                        if (!waitw(sh, &bar[TileBars::SCORES + (k & 1)], (k >> 1) & 1, kWhereTileScores)) return;
-                        tc_fence_after();
-                        // Blocks of 32 columns against this warp's 32 rows.  Where all columns are on the past (future)
-                        // side, a weight is the row's power times the column's; on the diagonal it is looked up by
-                        // distance; masked scores are selected away, not multiplied, for they may be anything.
+                for (int j = 0; j < w.nj; ++j, ++k) {
+                    const uint32_t tm_s = scores_at(k);
+                    const int cols = p.rev ? min(128, w.e - (w.t0 + 128 * j)) : 128;     // live columns
+                    if (!waitw(sh, &bar[TileBars::SCORES + (k & 1)], (k >> 1) & 1, kWhereTileScores)) return;
+                    tc_fence_after();
+                    // Blocks of 32 columns against this warp's 32 rows.  Where all columns are on the past (future)
+                    // side, a weight is the row's power times the column's; on the diagonal it is looked up by
+                    // distance; masked scores are selected away, not multiplied, for they may be anything.
 #pragma unroll 1
-                        for (int b = 0; b < 2; ++b) {
-                            const int cb = 2 * half + b, c1 = 32 * cb, d = j > 0 ? 1 : p.rev ? cb - quarter : quarter - cb;
-                            const uint32_t from = tm_s + lanes + c1, to = tm_s + lanes + 64 * half + 16 * b;
-                            uint32_t pk[16];
-                            if (d < 0) {
+                    for (int b = 0; b < 2; ++b) {
+                        const int cb = 2 * half + b, c1 = 32 * cb, d = j > 0 ? 1 : p.rev ? cb - quarter : quarter - cb;
+                        const uint32_t from = tm_s + lanes + c1, to = tm_s + lanes + 64 * half + 16 * b;
+                        uint32_t pk[16];
+                        if (d < 0) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) pk[i] = 0;
-                                tmem_st16(to, pk);
-                                continue;
-                            }
-                            float f = p.scale;
-                            if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
-                            else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
-                            if (d == 0 || c1 + 32 > cols) {
-                                // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
-                                const float *v = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
-                                const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
-#pragma unroll 1
-                                for (int g = 0; g < 32; g += 8) {
-                                    float x[8];
-                                    tmem_ld8(from + g, x);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) x[i] = g + i >= lo && g + i < hi ? x[i] * f * v[g + i] : 0.f;
-                                    tmem_st4(to + g / 2, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                             pack_bf16x2(x[6], x[7]));
-                                }
-                                continue;
-                            }
-                            float x[32];
-                            tmem_ld32(from, x);
-                            tmem_wait_ld();
-                            const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
-                            const float2 f2 = make_float2(f, f);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 v = w4[i / 4];
-                                const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(v.x, v.y));
-                                const float2 hi2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(v.z, v.w));
-                                pk[i / 2] = pack_bf16x2(lo2.x, lo2.y);
-                                pk[i / 2 + 1] = pack_bf16x2(hi2.x, hi2.y);
-                            }
+                            for (int i = 0; i < 16; ++i) pk[i] = 0;
                             tmem_st16(to, pk);
+                            continue;
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[TileBars::WEIGHTS + (k & 1)]);
+                        float f = p.scale;
+                        if (j > 0) f *= decay_pow(ld, 128 * (j - 1) + (p.rev ? 128 - r : r));
+                        else if (d > 0) f *= decay_pow(ld, p.rev ? c1 - r : r - c1 - 32);
+                        if (d == 0 || c1 + 32 > cols) {
+                            // the diagonal block, or one that the sequence ends in: columns lo .. hi - 1 are live
+                            const float *v = tab + (d > 0 ? (j > 0 ? c1 : p.rev ? 0 : 96) : p.rev ? -lane : 128 - lane);
+                            const int lo = d == 0 && p.rev ? lane : 0, hi = min(d == 0 && !p.rev ? lane + 1 : 32, cols - c1);
+#pragma unroll 1
+                            for (int g = 0; g < 32; g += 8) {
+                                float x[8];
+                                tmem_ld8(from + g, x);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] = g + i >= lo && g + i < hi ? x[i] * f * v[g + i] : 0.f;
+                                tmem_st4(to + g / 2, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                         pack_bf16x2(x[6], x[7]));
+                            }
+                            continue;
+                        }
+                        float x[32];
+                        tmem_ld32(from, x);
+                        tmem_wait_ld();
+                        const float4 *w4 = reinterpret_cast<const float4 *>(tab + (j > 0 ? c1 : p.rev ? 0 : 96));
+                        const float2 f2 = make_float2(f, f);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 v = w4[i / 4];
+                            const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), f2), make_float2(v.x, v.y));
+                            const float2 hi2 = __fmul2_rn(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f2), make_float2(v.z, v.w));
+                            pk[i / 2] = pack_bf16x2(lo2.x, lo2.y);
+                            pk[i / 2 + 1] = pack_bf16x2(hi2.x, hi2.y);
+                        }
+                        tmem_st16(to, pk);
                     }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[TileBars::WEIGHTS + (k & 1)]);
+                }
             }
         };
         run();
