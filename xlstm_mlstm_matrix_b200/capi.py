@@ -461,16 +461,31 @@ def bwd(q, k, v, i_pre, f_pre, dh, state=None, dstate=None, qk_scale=None, strea
 # ---- xlstm_layer.h: torch conveniences (checks, allocation, marshalling) ------------
 # These calls also serve single tokens, where the host's time is the call's time: shapes are compared as they
 # are, addresses go to ctypes as plain integers, and a shape's descriptor and workspace size are formed once.
+_torch = None          # the torch module, once a helper has been called (importing this module loads nothing)
+_current_stream = None     # CUDA device index -> its current stream's handle
+
+
+def _load_torch():
+    global _torch, _current_stream
+    import torch
+    # the handle without a stream object around it, where this torch offers it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+    _torch = torch
+    return torch
+
+
 def _want(x, name, shape, dtype, index):
     """x is a contiguous tensor of this shape and type on CUDA device `index`."""
+    if x.dtype == dtype and x.shape == shape and x.get_device() == index and x.is_contiguous():
+        return
     if x.dtype != dtype:
         raise TypeError(f"{name}: dtype {x.dtype}, expected {dtype}")
     if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
     if x.get_device() != index:
         raise ValueError(f"{name} is on {x.device}, expected CUDA device {index}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
 
 
 def _raw(x):
@@ -479,47 +494,42 @@ def _raw(x):
 
 def _run(fn, index, stream, *args):
     """fn(*args, stream) with device `index` current, on its current stream by default."""
-    import torch
     if index < 0:
         raise ValueError("CUDA tensors expected")
-    stream = torch.cuda.current_stream(index).cuda_stream if stream is None else \
-        stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    stream = _current_stream(index) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    if _torch.cuda.current_device() == index:
         st = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(index):
             st = fn(*args, stream)
     if st != XLSTM_OK:
         raise XlstmError(st, fn.__name__)
 
 
 @functools.lru_cache(maxsize=256)
-def _linattn_plan(B, H, T, dqk, dv, dtype, scale):
-    """The descriptor of a shape and its forward and backward workspace sizes."""
-    desc = make_linattn_desc(B, H, T, dqk, dv, dtype, scale)
-    return desc, max(256, xlstm_linattn_workspace_size(desc)), max(256, xlstm_linattn_bwd_workspace_size(desc))
+def _linattn_plan(q_shape, dv, dtype, scale):
+    """The descriptor of a shape, its forward and backward workspace sizes, and the shapes of v and of the state."""
+    B, H, T, dqk = q_shape if len(q_shape) == 4 else (*q_shape[:2], 1, q_shape[2])
+    desc = make_linattn_desc(B, H, T, dqk, dv, dtype, dqk ** -0.5 if scale is None else float(scale))
+    return (desc, max(256, xlstm_linattn_workspace_size(desc)), max(256, xlstm_linattn_bwd_workspace_size(desc)),
+            (*q_shape[:-1], dv), (B, H, dv, dqk), (B,), (H,))
 
 
-def _linattn_inputs(q, k, v, log_decay, state, lens, scale, token_axis):
-    import torch
-    dt, f32 = q.dtype, torch.float32
-    code = _dtype_code(q)
-    if q.dim() != 3 + token_axis or v.dim() != 3 + token_axis:
-        raise ValueError(f"q: {q.dim()} axes, v: {v.dim()} axes, expected {3 + token_axis}")
-    shape, dv = q.shape, v.shape[-1]
-    B, H, dqk = shape[0], shape[1], shape[-1]
-    index = q.get_device()
+def _linattn_inputs(q, k, v, log_decay, state, lens, scale, axes):
+    torch = _torch or _load_torch()
+    dt, shape, index = q.dtype, q.shape, q.get_device()
+    if len(shape) != axes or v.dim() != axes:
+        raise ValueError(f"q: {q.dim()} axes, v: {v.dim()} axes, expected {axes}")
+    plan = _linattn_plan(shape, v.shape[-1], _dtype_code(q), scale)
     _want(q, "q", shape, dt, index)
     _want(k, "k", shape, dt, index)
-    _want(v, "v", (*shape[:-1], dv), dt, index)
-    _want(log_decay, "log_decay", (H,), f32, index)
+    _want(v, "v", plan[3], dt, index)
+    _want(log_decay, "log_decay", plan[6], torch.float32, index)
     if state is not None:
-        _want(state, "state", (B, H, dv, dqk), f32, index)
+        _want(state, "state", plan[4], torch.float32, index)
     if lens is not None:
-        _want(lens, "lens", (B,), torch.int32, index)
-    plan = _linattn_plan(B, H, shape[2] if token_axis else 1, dqk, dv, code,
-                         dqk ** -0.5 if scale is None else float(scale))
-    return index, plan, (B, H, dv, dqk)
+        _want(lens, "lens", plan[5], torch.int32, index)
+    return torch, index, plan
 
 
 def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=None, workspace=None, out=None):
@@ -530,18 +540,17 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
     (zero), lens [B] int32 or None (padded batch: sequence b has lens[b] tokens, o is zero behind them); scale
     defaults to dqk ** -0.5.  Returns (o, C): o [B,H,T,dv] in q's type and the final state.
     out: (o, C) to write into; C may be None (not formed)."""
-    import torch
-    index, (desc, size, _), state_shape = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 1)
+    torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 4)
     if out is None:
-        o, C = torch.empty_like(v), torch.empty(state_shape, device=v.device, dtype=torch.float32)
+        o, C = torch.empty_like(v), torch.empty(plan[4], device=v.device, dtype=torch.float32)
     else:
         o, C = out
-        _want(o, "out[0]", v.shape, v.dtype, index)
+        _want(o, "out[0]", plan[3], v.dtype, index)
         if C is not None:
-            _want(C, "out[1]", state_shape, torch.float32, index)
+            _want(C, "out[1]", plan[4], torch.float32, index)
     if workspace is None:
-        workspace = torch.empty(size, device=v.device, dtype=torch.uint8)
-    _run(load().xlstm_linattn_fwd, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        workspace = torch.empty(plan[1], device=v.device, dtype=torch.uint8)
+    _run(load().xlstm_linattn_fwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), o.data_ptr(), _raw(C), workspace.data_ptr(), workspace.numel())
     return o, C
 
@@ -549,15 +558,14 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
 def linattn_step(q, k, v, log_decay, state, scale=None, stream=None, out=None, inplace=False):
     """One token per sequence through xlstm_linattn_step.  q, k [B,H,dqk], v [B,H,dv], state [B,H,dv,dqk].
     Returns (o, C'); inplace=True updates state itself.  out: (o, C') to write into."""
-    import torch
-    index, (desc, _, _), state_shape = _linattn_inputs(q, k, v, log_decay, state, None, scale, 0)
+    torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, None, scale, 3)
     if out is None:
         o, C = torch.empty_like(v), state if inplace else torch.empty_like(state)
     else:
         o, C = out[0], state if inplace else out[1]
-        _want(o, "out[0]", v.shape, v.dtype, index)
-        _want(C, "out[1]", state_shape, torch.float32, index)
-    _run(load().xlstm_linattn_step, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        _want(o, "out[0]", plan[3], v.dtype, index)
+        _want(C, "out[1]", plan[4], torch.float32, index)
+    _run(load().xlstm_linattn_step, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          state.data_ptr(), o.data_ptr(), C.data_ptr())
     return o, C
 
@@ -565,16 +573,15 @@ def linattn_step(q, k, v, log_decay, state, scale=None, stream=None, out=None, i
 def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lens=None, scale=None, stream=None, workspace=None):
     """Gradients of linattn_fwd through xlstm_linattn_bwd: do is the gradient of o (q's type), dstate that of the
     final state (fp32) or None.  Returns dict(dq, dk, dv, dC0): the inputs' types, dC0 fp32."""
-    import torch
-    index, (desc, _, size), state_shape = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 1)
-    _want(do, "do", v.shape, v.dtype, index)
+    torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 4)
+    _want(do, "do", plan[3], v.dtype, index)
     if dstate is not None:
-        _want(dstate, "dstate", state_shape, torch.float32, index)
+        _want(dstate, "dstate", plan[4], torch.float32, index)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dC0 = torch.empty(state_shape, device=v.device, dtype=torch.float32)
+    dC0 = torch.empty(plan[4], device=v.device, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(size, device=v.device, dtype=torch.uint8)
-    _run(load().xlstm_linattn_bwd, index, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        workspace = torch.empty(plan[2], device=v.device, dtype=torch.uint8)
+    _run(load().xlstm_linattn_bwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), do.data_ptr(), _raw(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
          dC0.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dict(dq=dq, dk=dk, dv=dv, dC0=dC0)
@@ -585,33 +592,32 @@ _ACTS = {"none": XLSTM_ACT_NONE, "silu": XLSTM_ACT_SILU, "sigmoid": XLSTM_ACT_SI
 
 
 @functools.lru_cache(maxsize=256)
-def _group_norm_plan(B, T, G, D, x_dtype, y_dtype, layout, act, eps):
-    """The descriptor of a shape and its backward workspace size."""
-    desc = make_group_norm_desc(B, T, G, D, x_dtype, y_dtype, layout, act, eps)
-    return desc, max(256, xlstm_group_norm_bwd_workspace_size(desc))
+def _group_norm_plan(x_shape, x_dtype, y_dtype, layout, act, eps):
+    """The descriptor of a shape, its backward workspace size, and the shapes of y and of the parameters."""
+    if layout not in _LAYOUTS or act not in _ACTS:
+        raise ValueError(f"layout {layout!r} (of {sorted(_LAYOUTS)}), act {act!r} (of {sorted(_ACTS)})")
+    if len(x_shape) != 4:
+        raise ValueError(f"x: {len(x_shape)} axes, expected 4")
+    code = {_torch.float32: XLSTM_F32, _torch.bfloat16: XLSTM_BF16}
+    if x_dtype not in code or y_dtype not in code:
+        raise TypeError(f"x and y must be bf16 or fp32, got {x_dtype} and {y_dtype}")
+    B, G, T, D = x_shape if layout == "heads" else (x_shape[0], x_shape[2], x_shape[1], x_shape[3])
+    desc = make_group_norm_desc(B, T, G, D, code[x_dtype], code[y_dtype], _LAYOUTS[layout], _ACTS[act], eps)
+    return desc, max(256, xlstm_group_norm_bwd_workspace_size(desc)), (B, T, G * D), (G * D,)
 
 
 def _group_norm_inputs(x, weight, bias, gate, act, layout, eps, y_dtype):
-    import torch
-    if layout not in _LAYOUTS or act not in _ACTS:
-        raise ValueError(f"layout {layout!r} (of {sorted(_LAYOUTS)}), act {act!r} (of {sorted(_ACTS)})")
-    code = {torch.float32: XLSTM_F32, torch.bfloat16: XLSTM_BF16}
-    if x.dtype not in code or y_dtype not in code:
-        raise TypeError(f"x and y must be bf16 or fp32, got {x.dtype} and {y_dtype}")
-    if x.dim() != 4:
-        raise ValueError(f"x: {x.dim()} axes, expected 4")
-    B, G, T, D = x.shape if layout == "heads" else (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
+    torch = _torch or _load_torch()
     index = x.get_device()
+    plan = _group_norm_plan(x.shape, x.dtype, y_dtype, layout, act, eps)
     _want(x, "x", x.shape, x.dtype, index)
     if weight is not None:
-        _want(weight, "weight", (G * D,), torch.float32, index)
+        _want(weight, "weight", plan[3], torch.float32, index)
     if bias is not None:
-        _want(bias, "bias", (G * D,), torch.float32, index)
-    shape = (B, T, G * D)
+        _want(bias, "bias", plan[3], torch.float32, index)
     if gate is not None:
-        _want(gate, "gate", shape, y_dtype, index)
-    plan = _group_norm_plan(B, T, G, D, code[x.dtype], code[y_dtype], _LAYOUTS[layout], _ACTS[act], eps)
-    return index, plan, shape
+        _want(gate, "gate", plan[2], y_dtype, index)
+    return torch, index, plan
 
 
 def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads", eps=1e-5, out_dtype=None, stream=None,
@@ -623,14 +629,13 @@ def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads",
     x [B,H,T,D] (layout "heads", as the cells write it) or [B,T,H,D] ("tokens"), bf16 or fp32; weight, bias [H*D]
     fp32 or None; gate [B,T,H*D] in the output's type.  Returns y [B,T,H*D] in out_dtype (the gate's type, else
     x's, by default)."""
-    import torch
     dt = out.dtype if out is not None else out_dtype if out_dtype is not None else gate.dtype if gate is not None else x.dtype
-    index, (desc, _), shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
+    torch, index, plan = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
     if out is None:
-        out = torch.empty(shape, device=x.device, dtype=dt)
+        out = torch.empty(plan[2], device=x.device, dtype=dt)
     else:
-        _want(out, "out", shape, dt, index)
-    _run(load().xlstm_group_norm, index, stream, desc, x.data_ptr(), _raw(weight), _raw(bias), _raw(gate), out.data_ptr())
+        _want(out, "out", plan[2], dt, index)
+    _run(load().xlstm_group_norm, index, stream, plan[0], x.data_ptr(), _raw(weight), _raw(bias), _raw(gate), out.data_ptr())
     return out
 
 
@@ -638,13 +643,12 @@ def group_norm_bwd(dy, x, weight=None, bias=None, gate=None, act="silu", layout=
                    workspace=None):
     """Gradients of group_norm through xlstm_group_norm_bwd: dict(dx, dgate, dweight, dbias); None in the place of
     what was not given."""
-    import torch
-    index, (desc, size), shape = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
-    _want(dy, "dy", shape, dy.dtype, index)
+    torch, index, plan = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
+    _want(dy, "dy", plan[2], dy.dtype, index)
     dx, dgate, dw, db = torch.empty_like(x), *(None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
     if workspace is None and (weight is not None or bias is not None):
-        workspace = torch.empty(size, device=x.device, dtype=torch.uint8)
-    _run(load().xlstm_group_norm_bwd, index, stream, desc, x.data_ptr(), _raw(weight), _raw(bias), _raw(gate),
+        workspace = torch.empty(plan[1], device=x.device, dtype=torch.uint8)
+    _run(load().xlstm_group_norm_bwd, index, stream, plan[0], x.data_ptr(), _raw(weight), _raw(bias), _raw(gate),
          dy.data_ptr(), dx.data_ptr(), _raw(dgate), _raw(dw), _raw(db), _raw(workspace),
          0 if workspace is None else workspace.numel())
     return dict(dx=dx, dgate=dgate, dweight=dw, dbias=db)

@@ -10,6 +10,7 @@ namespace xlstm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kChain = 64;        // threads of a chain block: small, so that a few heads' states spread over all SMs
 constexpr int kK = 32;            // inner-product columns of one step
 constexpr int kTile = 64 * kK;    // floats of a 64-row tile
 constexpr int kSeg = kSimtSegment;   // tokens of a segment: one output tile's rows
@@ -166,12 +167,12 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
 // memory (each element is read before it is written).  The factor l^{e_n-s_n} is held as two floats: over a
 // thousand segments one rounded factor would drift the oldest tokens' weight by a thousand of its roundings.
 template <typename S>
-__global__ void __launch_bounds__(kThreads) chain_kernel(const __grid_constant__ LinStates jobs) {
+__global__ void __launch_bounds__(kChain) chain_kernel(const __grid_constant__ LinStates jobs) {
     unsigned id;
     const LinStateP &p = jobs.p[job_of_block(jobs, id)];
     const size_t area = (size_t)p.dv * p.dqk;
-    const int per_head = (int)((area / 4 + kThreads - 1) / kThreads), bh = id / per_head;
-    const size_t el = ((size_t)(id % per_head) * kThreads + threadIdx.x) * 4;
+    const int per_head = (int)((area / 4 + kChain - 1) / kChain), bh = id / per_head;
+    const size_t el = ((size_t)(id % per_head) * kChain + threadIdx.x) * 4;
     if (el >= area) return;
     const int len = seq_len(p.lens, bh / p.H, p.T), nseg = (len + p.G - 1) / p.G;
     const float ld = head_log_decay(p.log_decay, bh % p.H);
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(const __grid_constant__
     S *out = static_cast<S *>(p.states) + (size_t)bh * p.nseg * area + el;
     float4 c = p.init ? load4(p.init + (size_t)bh * area + el) : make_float4(0.f, 0.f, 0.f, 0.f);
     const double full = exp((double)ld * p.G), tail = exp((double)ld * (len - (nseg - 1) * p.G));
-    constexpr int kAhead = 8;   // sums in flight
+    constexpr int kAhead = 16;   // sums in flight
     for (int i0 = 0; i0 < nseg; i0 += kAhead) {
         float4 u[kAhead];
 #pragma unroll
@@ -392,10 +393,10 @@ cudaError_t linattn_tile_simt(LinTiles jobs, int32_t *status, cudaStream_t s) {
 
 cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s) {
     const unsigned blocks = number_blocks(jobs, [](const LinStateP &p) {
-        return (size_t)p.B * p.H * (((size_t)p.dv * p.dqk / 4 + kThreads - 1) / kThreads);
+        return (size_t)p.B * p.H * (((size_t)p.dv * p.dqk / 4 + kChain - 1) / kChain);
     });
-    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(jobs);
-    else chain_kernel<float><<<blocks, kThreads, 0, s>>>(jobs);
+    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kChain, 0, s>>>(jobs);
+    else chain_kernel<float><<<blocks, kChain, 0, s>>>(jobs);
     return cudaGetLastError();
 }
 
