@@ -180,9 +180,10 @@ __global__ void __launch_bounds__(kChain) chain_kernel(const __grid_constant__ L
     S *out = static_cast<S *>(p.states) + (size_t)bh * p.nseg * area + el;
     float4 c = p.init ? load4(p.init + (size_t)bh * area + el) : make_float4(0.f, 0.f, 0.f, 0.f);
     const double full = exp((double)ld * p.G), tail = exp((double)ld * (len - (nseg - 1) * p.G));
-    constexpr int kAhead = 16;   // sums in flight
-    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-        float4 u[kAhead];
+    const float2 by_full = make_float2((float)full, (float)(full - (double)(float)full));
+    const float2 by_tail = make_float2((float)tail, (float)(tail - (double)(float)tail));
+    constexpr int kAhead = 8;   // sums on their way while as many are worked on
+    const auto fetch = [&](float4 (&u)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int n = p.rev ? nseg - 1 - (i0 + i) : i0 + i;
@@ -190,18 +191,27 @@ __global__ void __launch_bounds__(kChain) chain_kernel(const __grid_constant__ L
             // the last segment's sum only enters the final state
             if (i0 + i < nseg && (i0 + i + 1 < nseg || p.last)) u[i] = load4(U + (size_t)n * area);
         }
+    };
+    const auto chain = [&](const float4 (&u)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (i0 + i >= nseg) break;
             const int n = p.rev ? nseg - 1 - (i0 + i) : i0 + i;
             store4(out + (size_t)n * area, c);
-            const double f = n == nseg - 1 ? tail : full;
-            const float hi = (float)f, lo = (float)(f - (double)hi);
-            c.x = fmaf(c.x, hi, fmaf(c.x, lo, u[i].x));
-            c.y = fmaf(c.y, hi, fmaf(c.y, lo, u[i].y));
-            c.z = fmaf(c.z, hi, fmaf(c.z, lo, u[i].z));
-            c.w = fmaf(c.w, hi, fmaf(c.w, lo, u[i].w));
+            const float2 f = n == nseg - 1 ? by_tail : by_full;
+            c.x = fmaf(c.x, f.x, fmaf(c.x, f.y, u[i].x));
+            c.y = fmaf(c.y, f.x, fmaf(c.y, f.y, u[i].y));
+            c.z = fmaf(c.z, f.x, fmaf(c.z, f.y, u[i].z));
+            c.w = fmaf(c.w, f.x, fmaf(c.w, f.y, u[i].w));
         }
+    };
+    float4 u0[kAhead], u1[kAhead];
+    fetch(u0, 0);
+    for (int i0 = 0; i0 < nseg; i0 += 2 * kAhead) {
+        fetch(u1, i0 + kAhead);
+        chain(u0, i0);
+        fetch(u0, i0 + 2 * kAhead);
+        chain(u1, i0 + kAhead);
     }
     if (p.last) store4(p.last + (size_t)bh * area + el, c);
 }
