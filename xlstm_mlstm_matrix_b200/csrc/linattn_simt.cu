@@ -217,12 +217,12 @@ __global__ void __launch_bounds__(kChain) chain_kernel(const __grid_constant__ L
 }
 
 // ---- output tiles: 16 M of a segment's tokens x 64 N columns per block ---------------------------------------
-// Steps of kK inner-product columns, each step's operands copied while the one before is worked on: the
-// entering state's part (X against the state), the scores (X against Y), and the weighted scores against Z.
+// Steps of kK inner-product columns, each step's operands copied while the ones before are worked on: X against the
+// entering state and against Y (the scores), then the weighted scores against Z.
 template <int N>
 struct TileSmem {
-    static constexpr int STEP = (1 + N) * kTile;              // A tile, N B tiles
-    static constexpr int STEPS = 4;                            // 64, 96 or 160 KB: two blocks per SM at N = 1
+    static constexpr int STEP = (2 + N) * kTile;              // X, Y and N state tiles, or Z in the state's place
+    static constexpr int STEPS = N == 1 ? 3 : N == 2 ? 3 : 4;  // 72, 96 or 192 KB: two blocks per SM at N <= 2
     static constexpr int BYTES = 4 * (STEPS * STEP + 2 * kTile + kSeg + 4);    // steps, scores, powers
 };
 template <int M, int N>
@@ -251,24 +251,24 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
         const float *z = static_cast<const float *>(p.z) + ((size_t)bh * p.T + t0) * p.dz;
         const float *state = static_cast<const float *>(p.states) + ((size_t)bh * p.nseg + n) * p.dx * p.dz;
         const bool entry = p.rev ? (e < len || p.has_init) : (n > 0 || p.has_init);
-        const int nk = (p.dx + kK - 1) / kK, first = entry ? nk : 0, total = first + nk + 2;
+        const int nk = (p.dx + kK - 1) / kK, total = nk + 2;
         auto fetch = [&](int st) {
             if (st < total) {
-                float *A = sm + st % S::STEPS * S::STEP, *Bt = A + kTile;
-                if (st < first) {
+                float *A = sm + st % S::STEPS * S::STEP, *Yt = A + kTile, *Bt = Yt + kTile;
+                if (st < nk) {
                     copy_tile<R>(A, x, p.dx, rows - r0, st * kK, p.dx);
-                    if (p.state_t)
-                        copy_rows<kK, 64 * N>(Bt, state + (size_t)st * kK * p.dz, p.dz, p.dx - st * kK, z0, p.dz);
-                    else
+                    copy_tile<64>(Yt, y, p.dx, rows, st * kK, p.dx);
+                    if (entry) {
+                        if (p.state_t)
+                            copy_rows<kK, 64 * N>(Bt, state + (size_t)st * kK * p.dz, p.dz, p.dx - st * kK, z0, p.dz);
+                        else
 #pragma unroll
-                        for (int c = 0; c < N; ++c)
-                            copy_tile<64>(Bt + c * kTile, state + (size_t)(z0 + 64 * c) * p.dx, p.dx, p.dz - z0 - 64 * c,
-                                          st * kK, p.dx);
-                } else if (st < first + nk) {
-                    copy_tile<R>(A, x, p.dx, rows - r0, (st - first) * kK, p.dx);
-                    copy_tile<64>(Bt, y, p.dx, rows, (st - first) * kK, p.dx);
+                            for (int c = 0; c < N; ++c)
+                                copy_tile<64>(Bt + c * kTile, state + (size_t)(z0 + 64 * c) * p.dx, p.dx, p.dz - z0 - 64 * c,
+                                              st * kK, p.dx);
+                    }
                 } else {
-                    const int h = st - first - nk;
+                    const int h = st - nk;
                     copy_rows<kK, 64 * N>(Bt, z + (size_t)h * kK * p.dz, p.dz, rows - h * kK, z0, p.dz);
                 }
             }
@@ -282,24 +282,14 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
             copies_wait<S::STEPS - 2>();
             __syncthreads();
             fetch(st + S::STEPS - 1);     // into the buffer of the step before, which every thread has left
-            const float *A = sm + st % S::STEPS * S::STEP, *Bt = A + kTile;
-            if (st < first) {
-                if (p.state_t) product_nn<M, N>(acc, A, Bt, ty, tx);
-                else product_nt<M, N>(acc, A, Bt, ty, tx);
-                if (st == first - 1) {
-#pragma unroll
-                    for (int i = 0; i < M; ++i) {
-                        const int r = r0 + M * ty + i;
-                        const float rho = p.rev ? pw[max(rows - 1 - r, 0)] : p.scale * pw[r + 1];
-#pragma unroll
-                        for (int c = 0; c < N; ++c)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[c][i][j] *= rho;
-                    }
+            const float *A = sm + st % S::STEPS * S::STEP, *Yt = A + kTile, *Bt = Yt + kTile;
+            if (st < nk) {
+                product_nt<M, 1>(sc, A, Yt, ty, tx);
+                if (entry) {
+                    if (p.state_t) product_nn<M, N>(acc, A, Bt, ty, tx);
+                    else product_nt<M, N>(acc, A, Bt, ty, tx);
                 }
-            } else if (st < first + nk) {
-                product_nt<M, 1>(sc, A, Bt, ty, tx);
-                if (st == first + nk - 1) {
+                if (st == nk - 1) {
                     // token s = 4 tx + j is float4 tx of row t: tile tx / 8, column group tx mod 8
 #pragma unroll
                     for (int i = 0; i < M; ++i) {
@@ -310,10 +300,16 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
                             w[j] = far >= 0 && s < rows ? p.scale * pw[far] * sc[0][i][j] : 0.f;
                         }
                         store4(Ps + (tx >> 3) * kTile + at(M * ty + i, tx & 7), make_float4(w[0], w[1], w[2], w[3]));
+                        const int r = r0 + M * ty + i;
+                        const float rho = p.rev ? pw[max(rows - 1 - r, 0)] : p.scale * pw[r + 1];
+#pragma unroll
+                        for (int c = 0; c < N; ++c)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[c][i][j] *= rho;
                     }
                 }
             } else {
-                product_nn<M, N>(acc, Ps + (st - first - nk) * kTile, Bt, ty, tx);
+                product_nn<M, N>(acc, Ps + (st - nk) * kTile, Bt, ty, tx);
             }
         }
         copies_wait<0>();
