@@ -4,8 +4,8 @@
 // issued as tcgen05.mma by one thread, accumulated in tensor memory in fp32.
 //
 // state_tc_kernel: U_n = sum_s w_s z_s y_s^T, 128 z rows x NX y columns per block, 32 tokens a stage, chained over
-//   the segments where there are blocks enough.  The weighted rows w_s z_s enter as three bf16 parts: the final state
-//   leaves in fp32, one part would leave 2^-8 of each term and two 2^-16.
+//   the segments where there are blocks enough.  The weighted rows w_s z_s enter as bf16 parts, two where only entering
+//   states are wanted, three where the chain's end leaves in fp32 (state_parts).
 // tile_tc_kernel: 128 tokens x NZ output columns per tile.  The tile's own rows X stay in shared memory; Y, Z and the
 //   entering state pass through a ring of 16 KB units.  Per 128 tokens of the segment the scores X Y^T land in tensor
 //   memory, are weighted with powers of the decay and written back as one bf16 copy (each rounding is relative to its
@@ -51,12 +51,9 @@ constexpr int kPart = 128 * kStep * 2;   // one part of the weighted rows: 8 KB
 
 template <int NX, bool SEQ>
 struct StateCfg {
-    // NX = 256: the state and the sum fill tensor memory, and the products wait while a sum is folded in.  NX <= 128: the
-    // state lives in registers, and two sums take turns.
-    static constexpr bool IN_TMEM = NX == 256;
-    static constexpr int ACCS = IN_TMEM ? 1 : 2;
+    static constexpr int ACCS = 2;      // two sums take turns in tensor memory
     // Loads run this many stages ahead (about 2000 cycles of latency against 400 to 800 of products a stage).
-    static constexpr int STAGES = IN_TMEM ? 4 : 6, PARTS = IN_TMEM || !(SEQ || NX == 64) ? 2 : 3;
+    static constexpr int STAGES = NX == 256 ? 4 : 6, PARTS = NX == 256 || !(SEQ || NX == 64) ? 2 : 3;
     static constexpr int Y_BYTES = NX * kStep * 2;
     static constexpr int STAGE = kPart + Y_BYTES;               // z and y as they come
     static constexpr int OFF_PARTS = STAGES * STAGE, PARTS_BYTES = 3 * kPart;
@@ -68,11 +65,18 @@ struct StateCfg {
                          B_LAST = B_RAW + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * (B_LAST + 1);
     static constexpr int BYTES = OFF_MISC + 16;
-    static constexpr int STATE = NX;                            // state's first column (IN_TMEM)
-    static constexpr int COLS = 2 * NX;
+    static constexpr int COLS = ACCS * NX;
 };
 constexpr int kStateThreads = 640;       // TMA, MMA, two idle warps; two groups of four warps of weights; eight fold warps
 constexpr int kFold = 384;               // first thread of the fold warps
+// Registers per thread of the three kinds, out of the 96 each that 640 threads are launched with: the state lives in the
+// fold warps' (128 of them with NX = 256).
+constexpr int kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
+static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * 96, "no more than the launch brought");
+
+// Parts of the weighted rows.  Two leave 2^-16 of each term at most, far below the 2^-9 that an entering state is rounded to
+// anyway; three are the fp32 product exactly, for a final state that leaves in fp32.
+__device__ __forceinline__ int state_parts(const LinStateP &p) { return p.last ? 3 : 2; }
 
 // One tile's walk over its segments, the same in every role.
 struct StatePlan {
@@ -84,9 +88,9 @@ struct StateWalk {
     int first;                           // SUM: the block's only segment
     float ld;
 };
-// (Not inlined, for the kernel's code size; its divisions are products.)
+// (Inlined, like the waits: with registers moved between warps the kernel can call no function.)
 template <int NX, bool SEQ>
-__device__ __noinline__ StateWalk state_walk(const LinStateP &p, const StatePlan &pl, int item) {
+__device__ __forceinline__ StateWalk state_walk(const LinStateP &p, const StatePlan &pl, int item) {
     StateWalk w;
     int rest = quotient(item, pl.by_ytiles);
     w.y0 = (item - rest * (int)pl.by_ytiles.d) * NX;
@@ -151,6 +155,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     tc_fence_after();
     const uint32_t tm = *tmem_slot;
 
+    if (warp < 4) set_registers<kIoRegs, false>();
+    else if (warp < 12) set_registers<kWeightRegs, false>();
+    else set_registers<kFoldRegs, true>();
+
     if (warp < 4) {
         if (warp == 0) {
             // ===================== loads =====================
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                     for (int t = s0; t < e; t += kStep, ++c) {
                         const int st = c % C::STAGES;
-                        if (c >= C::STAGES && !waitw(sh, &bar[C::B_EMPTY + st], (c / C::STAGES - 1) & 1, kWhereSumEmpty)) {
+                        if (c >= C::STAGES && !wait_inline(sh, &bar[C::B_EMPTY + st], (c / C::STAGES - 1) & 1, kWhereSumEmpty)) {
                             go = false;
                             break;
                         }
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                             for (int b = 0; b < NX / 64; ++b) tma_load_3d(Ys + 4096 * b, &tmy, landed, w.y0 + 64 * b, t, w.bh);
                         }
                         if (ends) {
-                            if (!waitw(sh, landed, raw & 1, kWhereSumRaw)) {
+                            if (!wait_inline(sh, landed, raw & 1, kWhereSumRaw)) {
                                 go = false;
                                 break;
                             }
@@ -199,6 +207,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             // The whole warp walks the work, so that descriptors stay uniform; one lane issues.
             constexpr uint32_t id_u = make_idesc(128, NX, kFmtBF16, kFmtBF16, 1, 1);
             const bool leader = elect_one();
+            const int nq = state_parts(p);
             const auto run = [&]() {
                 RingAt at, part;
                 int g = 0;          // segments summed
@@ -207,10 +216,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     for (int k = 0; k < w.nm; ++k, ++g) {
                         const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                         const uint32_t acc = tm + g % C::ACCS * NX;
-                        if (g >= C::ACCS && !waitw(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken))
+                        if (g >= C::ACCS && !wait_inline(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken))
                             return;
                         for (int t = s0; t < e; t += kStep) {
-                            if (!waitw(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
+                            if (!wait_inline(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
                             tc_fence_after();
                             const uint64_t z = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
                             const uint64_t y = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE + kPart), 4096, 1024);
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                                 for (int ks = 0; ks < kStep / 16; ++ks)
 #pragma unroll
                                     for (int q = 0; q < 3; ++q)
-                                        mma_f16_ss(acc, z + (uint32_t)((q * kPart + ks * 2048) >> 4),
+                                        if (q < nq) mma_f16_ss(acc, z + (uint32_t)((q * kPart + ks * 2048) >> 4),
                                                    y + (uint32_t)(ks * 2048 >> 4), id_u, t > s0 || ks > 0 || q > 0);
                                 tc_commit(&bar[C::B_EMPTY + at.slot]);
                             }
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     } else if (warp < 12) {
         // ===================== weights =====================
         // the two groups take every other stage
-        const int t128 = tid & 127, group = (warp - 4) >> 2;
+        const int t128 = tid & 127, group = (warp - 4) >> 2, nq = state_parts(p);
         int c = 0;
         bool go = true;
         for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         const int s = t + t128 / 8 + 16 * i;
                         wt[i] = s < e ? (p.rev ? p.scale * decay_pow(ld, s - s0 + 1) : decay_pow(ld, e - 1 - s)) : 0.f;
                     }
-                    if (!waitw(sh, &bar[C::B_FULL + st], (c / C::STAGES) & 1, kWhereSumFull)) {
+                    if (!wait_inline(sh, &bar[C::B_FULL + st], (c / C::STAGES) & 1, kWhereSumFull)) {
                         go = false;
                         break;
                     }
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4 *>(Zs + 16 * (t128 + 128 * i));
                     // the products of the stage PARTS ago have read the parts' place
-                    if (c >= C::PARTS && !waitw(sh, &bar[C::B_EMPTY + (c - C::PARTS) % C::STAGES],
+                    if (c >= C::PARTS && !wait_inline(sh, &bar[C::B_EMPTY + (c - C::PARTS) % C::STAGES],
                                                 ((c - C::PARTS) / C::STAGES) & 1, kWhereSumParts)) {
                         go = false;
                         break;
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         split_scaled(u[i], wt[i & 1], part);
 #pragma unroll
                         for (int q = 0; q < 3; ++q)
-                            *reinterpret_cast<uint4 *>(parts + q * kPart + 16 * (t128 + 128 * i)) = part[q];
+                            if (q < nq) *reinterpret_cast<uint4 *>(parts + q * kPart + 16 * (t128 + 128 * i)) = part[q];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -302,14 +311,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (stores > 0) tma_store_wait();
                 mbar_arrive(&bar[C::B_OUT_FREE]);
             }
-            return waitw(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
+            return wait_inline(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
         };
         const auto store = [&](int slot, int z0, int y0) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::B_OUT_FULL]);
             if (warp == kFold / 32) {
-                if (!waitw(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
+                if (!wait_inline(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
                 constexpr int W = SEQ ? 64 : 32;    // columns of a box
                 if (lane == 0) {
                     for (int b = 0; b < NX / W; ++b)
@@ -330,32 +339,25 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 const size_t own = ((size_t)w.bh * p.dv + w.z0 + r) * p.dqk + w.y0 + half * CH;   // this thread's columns
                 const bool row = w.z0 + r < p.dv;
                 const auto inside = [&](int i) { return row && w.y0 + half * CH + i < p.dqk; };
-                // the state, 32 columns at a time: registers, or this thread's lane of tensor memory
-                constexpr int KEPT = C::IN_TMEM ? 1 : CH / 32;
-                float x[KEPT][32];
+                // the state, 32 columns at a time
+                float x[CH / 32][32];
 #pragma unroll
                 for (int c0 = 0; c0 < CH; c0 += 32) {
-                    float(&v)[32] = x[c0 / 32 % KEPT];
+                    float(&v)[32] = x[c0 / 32];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (p.init && inside(c0 + i)) u = *reinterpret_cast<const float4 *>(p.init + own + c0 + i);
                         v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
                     }
-                    if (C::IN_TMEM) tmem_st32(own_tm + C::STATE + c0, v);
                 }
-                if (C::IN_TMEM) tmem_wait_st();
                 for (int k = 0; go && k < w.nseg; ++k) {
                     const int n = segment_of<SEQ>(p, w, k);
                     if (k > 0 || p.init) {      // the state entering segment n
                         if (!(go = staging_free())) break;
 #pragma unroll
                         for (int c0 = 0; c0 < CH; c0 += 32) {
-                            float(&v)[32] = x[c0 / 32 % KEPT];
-                            if (C::IN_TMEM) {
-                                tmem_ld32(own_tm + C::STATE + c0, v);
-                                tmem_wait_ld();
-                            }
+                            float(&v)[32] = x[c0 / 32];
 #pragma unroll
                             for (int i = 0; i < 32; i += 8) {
                                 const int col = half * CH + c0 + i;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         if (!(go = store(w.bh * p.nseg + n, w.z0, w.y0))) break;
                     }
                     if (k >= w.nm) break;
-                    if (!waitw(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
+                    if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
                         go = false;
                         break;
                     }
@@ -375,40 +377,25 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     const float hi = n == w.nseg - 1 ? f.z : f.x, lo = n == w.nseg - 1 ? f.w : f.y;
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 32) {
-                        float(&v)[32] = x[c0 / 32 % KEPT];
-                        if (C::IN_TMEM) {       // both reads at once: the products wait for this loop
-                            float u[32];
-                            tmem_ld32(own_tm + C::STATE + c0, v);
-                            tmem_ld32(own_tm + c0, u);
+                        float(&v)[32] = x[c0 / 32];
+#pragma unroll
+                        for (int c1 = 0; c1 < 32; c1 += 8) {
+                            float u[8];
+                            tmem_ld8(own_tm + g % C::ACCS * NX + c0 + c1, u);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], hi, fmaf(v[i], lo, u[i]));
-                            tmem_st32(own_tm + C::STATE + c0, v);
-                        } else {
-#pragma unroll
-                            for (int c1 = 0; c1 < 32; c1 += 16) {
-                                float u[16];
-                                tmem_ld16(own_tm + g % C::ACCS * NX + c0 + c1, u);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) v[c1 + i] = fmaf(v[c1 + i], hi, fmaf(v[c1 + i], lo, u[i]));
-                            }
+                            for (int i = 0; i < 8; ++i) v[c1 + i] = fmaf(v[c1 + i], hi, fmaf(v[c1 + i], lo, u[i]));
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
-                    if (C::IN_TMEM) tmem_wait_st();
                     ++g;
                 }
                 if (go && p.last) {
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 32) {
-                        float(&v)[32] = x[c0 / 32 % KEPT];
-                        if (C::IN_TMEM) {
-                            tmem_ld32(own_tm + C::STATE + c0, v);
-                            tmem_wait_ld();
-                        }
+                        float(&v)[32] = x[c0 / 32];
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             if (inside(c0 + i))
@@ -416,7 +403,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     }
                 }
             } else if (w.nm) {
-                if (!waitw(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
+                if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
                     go = false;
                     break;
                 }

@@ -33,6 +33,28 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p != 0;
 }
+// The warpgroup's registers per thread from here on: gives some back, or takes from what others gave (and waits for it).
+// A kernel that does so calls no function (a function's code is compiled for one count of registers).
+template <int N, bool TAKE>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (TAKE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// waitw without a call.
+__device__ __forceinline__ bool wait_inline(const Shared &sh, uint64_t *bar, uint32_t parity, int where) {
+    bool done = mbar_try_wait(bar, parity);
+    if (!done) {
+        const uint64_t t0 = global_timer_ns();
+        while (!(done = mbar_try_wait_suspend(bar, parity, 20000))) {
+            if (*sh.abort_flag) break;
+            if (global_timer_ns() - t0 > kTimeoutNs) {
+                record_timeout(sh, where);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, done);
+}
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until this thread's stores have read their shared memory.
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -63,7 +85,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
 
 // l^n and l^m as two floats each: (l^n high, rest, l^m high, rest).  One rounded factor, applied once per segment,
 // would drift the oldest tokens' weight by a thousand of its roundings.
-__device__ __noinline__ float4 decay_factors(float ld, int n, int m) {
+__device__ __forceinline__ float4 decay_factors(float ld, int n, int m) {
     const double a = exp((double)ld * n), b = exp((double)ld * m);
     return make_float4((float)a, (float)(a - (double)(float)a), (float)b, (float)(b - (double)(float)b));
 }
