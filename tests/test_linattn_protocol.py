@@ -32,7 +32,7 @@ def test_two_relays_are_too_few():
     assert any(any("overrun" in p and "ZREADY" in p for p in f) for f in found)
 
 
-@pytest.mark.parametrize("stages,parts,accs", [(4, 2, 1), (4, 2, 2), (6, 3, 2), (6, 2, 2)])
+@pytest.mark.parametrize("stages,parts,accs", [(4, 2, 1), (4, 2, 2), (6, 3, 2), (6, 2, 2), (8, 4, 2)])
 @pytest.mark.parametrize("segments", [[[1]], [[8, 8, 3]], [[4], [4], [1]], [[16, 16], [16, 5], [2]], [[1, 1, 1, 1]] * 3], ids=str)
 @pytest.mark.parametrize("skip_last", [False, True])
 def test_state_kernel(stages, parts, accs, segments, skip_last):

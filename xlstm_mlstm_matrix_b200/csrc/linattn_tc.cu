@@ -52,13 +52,15 @@ constexpr int kPart = 128 * kStep * 2;   // one part of the weighted rows: 8 KB
 template <int NX, bool SEQ>
 struct StateCfg {
     static constexpr int ACCS = 2;      // two sums take turns in tensor memory
-    // Loads run this many stages ahead (about 2000 cycles of latency against 400 to 800 of products a stage).
-    static constexpr int STAGES = NX == 256 ? 4 : 6, PARTS = NX == 256 || !(SEQ || NX == 64) ? 2 : 3;
+    // A place holds a stage from the start of its loads (some 2000 cycles) through its weighting (as long) to the end of
+    // its products (400 to 800).  The first part takes the place of z; the others have PARTS places of their own.
+    static constexpr int STAGES = NX == 256 || (!SEQ && NX == 128) ? 6 : 8, PARTS = STAGES / 2;
     static constexpr int Y_BYTES = NX * kStep * 2;
     static constexpr int STAGE = kPart + Y_BYTES;               // z and y as they come
-    static constexpr int OFF_PARTS = STAGES * STAGE, PARTS_BYTES = 3 * kPart;
+    static constexpr int OFF_PARTS = STAGES * STAGE, PARTS_BYTES = 2 * kPart;
     static constexpr int OFF_OUT = OFF_PARTS + PARTS * PARTS_BYTES;
-    static constexpr int OUT = 128 * NX * (SEQ ? 2 : 4);        // what a store leaves from
+    static constexpr int ROUNDS = NX == 256 ? 2 : 1;            // a tile leaves in this many stores
+    static constexpr int OUT = 128 * NX * (SEQ ? 2 : 4) / ROUNDS;
     static constexpr int OFF_BAR = OFF_OUT + OUT;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_SCALED = 2 * STAGES, B_ACC = 3 * STAGES, B_TAKEN = B_ACC + 2,
                          B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_RAW = B_OUT_FREE + 1,
@@ -221,14 +223,15 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         for (int t = s0; t < e; t += kStep) {
                             if (!wait_inline(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
                             tc_fence_after();
-                            const uint64_t z = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
+                            const uint64_t z = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE), 4096, 1024);
+                            const uint64_t rest = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
                             const uint64_t y = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE + kPart), 4096, 1024);
                             if (leader) {
 #pragma unroll
                                 for (int ks = 0; ks < kStep / 16; ++ks)
 #pragma unroll
                                     for (int q = 0; q < 3; ++q)
-                                        if (q < nq) mma_f16_ss(acc, z + (uint32_t)((q * kPart + ks * 2048) >> 4),
+                                        if (q < nq) mma_f16_ss(acc, (q == 0 ? z : rest + (uint32_t)((q - 1) * kPart >> 4)) + (uint32_t)(ks * 2048 >> 4),
                                                    y + (uint32_t)(ks * 2048 >> 4), id_u, t > s0 || ks > 0 || q > 0);
                                 tc_commit(&bar[C::B_EMPTY + at.slot]);
                             }
@@ -271,11 +274,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         go = false;
                         break;
                     }
-                    const uint8_t *Zs = sm + st * C::STAGE;
+                    uint8_t *Zs = sm + st * C::STAGE;
                     uint8_t *parts = sm + C::OFF_PARTS + c % C::PARTS * C::PARTS_BYTES;
                     uint4 u[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4 *>(Zs + 16 * (t128 + 128 * i));
+                    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<uint4 *>(Zs + 16 * (t128 + 128 * i));
                     // the products of the stage PARTS ago have read the parts' place
                     if (c >= C::PARTS && !wait_inline(sh, &bar[C::B_EMPTY + (c - C::PARTS) % C::STAGES],
                                                 ((c - C::PARTS) / C::STAGES) & 1, kWhereSumParts)) {
@@ -288,7 +291,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         split_scaled(u[i], wt[i & 1], part);
 #pragma unroll
                         for (int q = 0; q < 3; ++q)
-                            if (q < nq) *reinterpret_cast<uint4 *>(parts + q * kPart + 16 * (t128 + 128 * i)) = part[q];
+                            if (q < nq)
+                                *reinterpret_cast<uint4 *>((q == 0 ? Zs : parts + (q - 1) * kPart) + 16 * (t128 + 128 * i)) = part[q];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             }
             return wait_inline(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
         };
-        const auto store = [&](int slot, int z0, int y0) {
+        const auto store = [&](int slot, int z0, int y0, int round) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::B_OUT_FULL]);
@@ -321,8 +325,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (!wait_inline(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
                 constexpr int W = SEQ ? 64 : 32;    // columns of a box
                 if (lane == 0) {
-                    for (int b = 0; b < NX / W; ++b)
-                        if (y0 + W * b < p.dqk) tma_store_3d(&tmo, out + b * 16384, y0 + W * b, z0, slot);
+                    for (int b = 0; b < NX / W / C::ROUNDS; ++b) {
+                        // (two rounds: one box of each half)
+                        const int y = y0 + W * (C::ROUNDS == 1 ? b : 2 * b + round);
+                        if (y < p.dqk) tma_store_3d(&tmo, out + b * 16384, y, z0, slot);
+                    }
                     tma_store_commit();
                 }
                 __syncwarp();
@@ -354,19 +361,23 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int k = 0; go && k < w.nseg; ++k) {
                     const int n = segment_of<SEQ>(p, w, k);
                     if (k > 0 || p.init) {      // the state entering segment n
-                        if (!(go = staging_free())) break;
 #pragma unroll
-                        for (int c0 = 0; c0 < CH; c0 += 32) {
-                            float(&v)[32] = x[c0 / 32];
+                        for (int round = 0; round < C::ROUNDS; ++round) {
+                            if (!(go = staging_free())) break;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                const int col = half * CH + c0 + i;
-                                *reinterpret_cast<uint4 *>(out + (col / 64) * 16384 + sw128_offset(r, (col % 64) / 8)) =
-                                    make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                                               pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+                            for (int c0 = 0; c0 < CH / C::ROUNDS; c0 += 32) {
+                                const float(&v)[32] = x[(round * (CH / C::ROUNDS) + c0) / 32];
+#pragma unroll
+                                for (int i = 0; i < 32; i += 8) {
+                                    const int col = half * (CH / C::ROUNDS) + c0 + i;      // of this round
+                                    *reinterpret_cast<uint4 *>(out + (col / 64) * 16384 + sw128_offset(r, (col % 64) / 8)) =
+                                        make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                                                   pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+                                }
                             }
+                            if (!(go = store(w.bh * p.nseg + n, w.z0, w.y0, round))) break;
                         }
-                        if (!(go = store(w.bh * p.nseg + n, w.z0, w.y0))) break;
+                        if (!go) break;
                     }
                     if (k >= w.nm) break;
                     if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                 ++g;
-                go = store(w.bh * p.nseg + w.first, w.z0, w.y0);
+                go = store(w.bh * p.nseg + w.first, w.z0, w.y0, 0);
             }
         }
         if (tid == kFold) tma_store_wait();
