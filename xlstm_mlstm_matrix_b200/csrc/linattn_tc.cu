@@ -59,8 +59,10 @@ struct StateCfg {
     static constexpr int STAGE = kPart + Y_BYTES;               // z and y as they come
     static constexpr int OFF_PARTS = STAGES * STAGE, PARTS_BYTES = 2 * kPart;
     static constexpr int OFF_OUT = OFF_PARTS + PARTS * PARTS_BYTES;
-    static constexpr int ROUNDS = NX == 256 ? 2 : 1;            // a tile leaves in this many stores
-    static constexpr int OUT = 128 * NX * (SEQ ? 2 : 4) / ROUNDS;
+    // What a store leaves from, boxes of 128 rows x 128 bytes.  SEQ: an entering state leaves in ROUNDS stores, the final
+    // one in NX / 64, of one box of each half.
+    static constexpr int ROUNDS = NX == 256 ? 2 : 1;
+    static constexpr int OUT = SEQ ? 32768 : 128 * NX * 4;
     static constexpr int OFF_BAR = OFF_OUT + OUT;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_SCALED = 2 * STAGES, B_ACC = 3 * STAGES, B_TAKEN = B_ACC + 2,
                          B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_RAW = B_OUT_FREE + 1,
@@ -122,8 +124,8 @@ __device__ __forceinline__ int segment_of(const LinStateP &p, const StateWalk &w
 template <int NX, bool SEQ>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_tc_kernel(const __grid_constant__ CUtensorMap tmz, const __grid_constant__ CUtensorMap tmy,
-                    const __grid_constant__ CUtensorMap tmo, const __grid_constant__ LinStateP p,
-                    const __grid_constant__ StatePlan pl, int32_t *status) {
+                    const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tml,
+                    const __grid_constant__ LinStateP p, const __grid_constant__ StatePlan pl, int32_t *status) {
     using C = StateCfg<NX, SEQ>;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
@@ -253,35 +255,44 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         // ===================== weights =====================
         // the two groups take every other stage
         const int t128 = tid & 127, group = (warp - 4) >> 2, nq = state_parts(p);
-        int c = 0;
+        const int row = t128 / 8;       // of a stage; the thread's 16-byte chunks are in rows row and row + 16
+        int c = 0, st = group, pp = group, phase = 0;      // stages so far; places of this group's next one and its parity
         bool go = true;
         for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
             const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
             const float ld = w.ld;
+            // the weights of a stage: a power per stage times these (one rounding more than the power itself)
+            const float own[2] = {p.rev ? p.scale * decay_pow(ld, row + 1) : decay_pow(ld, kStep - 1 - row),
+                                  p.rev ? p.scale * decay_pow(ld, row + 17) : decay_pow(ld, kStep - 17 - row)};
             for (int k = 0; go && k < w.nm; ++k) {
                 const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
-                for (int t = s0; t < e; t += kStep, ++c) {
-                    const int st = c % C::STAGES;
-                    if ((c & 1) != group) continue;
-                    // 16-byte chunks t128 + 128 i: token t128 / 8 of the upper half, or 16 further
-                    float wt[2];
+                const int first = s0 + ((c ^ group) & 1) * kStep;
+                c += (e - s0 + kStep - 1) / kStep;
+                for (int t = first; t < e; t += 2 * kStep) {
+                    const int left = e - kStep - t;     // tokens behind the stage; below 0 it is cut short
+                    const float base = decay_pow(ld, p.rev ? t - s0 : max(left, 0));
+                    float wt[2] = {base * own[0], base * own[1]};
+                    if (left < 0) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int s = t + t128 / 8 + 16 * i;
-                        wt[i] = s < e ? (p.rev ? p.scale * decay_pow(ld, s - s0 + 1) : decay_pow(ld, e - 1 - s)) : 0.f;
+                        for (int i = 0; i < 2; ++i) {
+                            const int n = e - 1 - t - row - 16 * i;
+                            if (!p.rev) wt[i] = decay_pow(ld, max(n, 0));
+                            if (n < 0) wt[i] = 0.f;
+                        }
                     }
-                    if (!wait_inline(sh, &bar[C::B_FULL + st], (c / C::STAGES) & 1, kWhereSumFull)) {
+                    if (!wait_inline(sh, &bar[C::B_FULL + st], phase, kWhereSumFull)) {
                         go = false;
                         break;
                     }
                     uint8_t *Zs = sm + st * C::STAGE;
-                    uint8_t *parts = sm + C::OFF_PARTS + c % C::PARTS * C::PARTS_BYTES;
+                    uint8_t *parts = sm + C::OFF_PARTS + pp * C::PARTS_BYTES;
                     uint4 u[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<uint4 *>(Zs + 16 * (t128 + 128 * i));
-                    // the products of the stage PARTS ago have read the parts' place
-                    if (c >= C::PARTS && !wait_inline(sh, &bar[C::B_EMPTY + (c - C::PARTS) % C::STAGES],
-                                                ((c - C::PARTS) / C::STAGES) & 1, kWhereSumParts)) {
+                    // the products of the stage PARTS ago have read the place of the parts
+                    // (none before the first PARTS stages: a barrier's phase before its first counts as over)
+                    const bool wrapped = st < C::PARTS;
+                    if (!wait_inline(sh, &bar[C::B_EMPTY + st + (wrapped ? C::STAGES : 0) - C::PARTS], phase ^ wrapped, kWhereSumParts)) {
                         go = false;
                         break;
                     }
@@ -297,6 +308,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[C::B_SCALED + st]);
+                    if ((st += 2) >= C::STAGES) {
+                        st -= C::STAGES;
+                        phase ^= 1;
+                    }
+                    if ((pp += 2) >= C::PARTS) pp -= C::PARTS;
                 }
             }
         }
@@ -317,19 +333,16 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             }
             return wait_inline(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
         };
-        const auto store = [&](int slot, int z0, int y0, int round) {
+        // Boxes b = 0 .. n - 1 of the staging memory to columns y + step b.
+        const auto store = [&](const CUtensorMap &map, int slot, int z0, int y, int step, int n) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::B_OUT_FULL]);
             if (warp == kFold / 32) {
                 if (!wait_inline(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
-                constexpr int W = SEQ ? 64 : 32;    // columns of a box
                 if (lane == 0) {
-                    for (int b = 0; b < NX / W / C::ROUNDS; ++b) {
-                        // (two rounds: one box of each half)
-                        const int y = y0 + W * (C::ROUNDS == 1 ? b : 2 * b + round);
-                        if (y < p.dqk) tma_store_3d(&tmo, out + b * 16384, y, z0, slot);
-                    }
+                    for (int b = 0; b < n; ++b)
+                        if (y + step * b < p.dqk) tma_store_3d(&map, out + b * 16384, y + step * b, z0, slot);
                     tma_store_commit();
                 }
                 __syncwarp();
@@ -375,7 +388,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                                                    pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
                                 }
                             }
-                            if (!(go = store(w.bh * p.nseg + n, w.z0, w.y0, round))) break;
+                            // (two rounds: one box of each half)
+                            if (!(go = store(tmo, w.bh * p.nseg + n, w.z0, w.y0 + 64 * round, 64 * C::ROUNDS, NX / 64 / C::ROUNDS))) break;
                         }
                         if (!go) break;
                     }
@@ -406,11 +420,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (go && p.last) {
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 32) {
-                        float(&v)[32] = x[c0 / 32];
+                        if (!(go = staging_free())) break;
+                        const float(&v)[32] = x[c0 / 32];
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            if (inside(c0 + i))
-                                *reinterpret_cast<float4 *>(p.last + own + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            *reinterpret_cast<float4 *>(out + half * 16384 + sw128_offset(r, i / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        if (!(go = store(tml, w.bh, w.z0, w.y0 + c0, CH, 2))) break;
                     }
                 }
             } else if (w.nm) {
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                 ++g;
-                go = store(w.bh * p.nseg + w.first, w.z0, w.y0, 0);
+                go = store(tmo, w.bh * p.nseg + w.first, w.z0, w.y0, 32, NX / 32);
             }
         }
         if (tid == kFold) tma_store_wait();
@@ -951,11 +966,16 @@ template <int NX, bool SEQ>
 cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
     using C = StateCfg<NX, SEQ>;
     const uint64_t BH = (uint64_t)p.B * p.H;
-    CUtensorMap tmz, tmy, tmo;
+    CUtensorMap tmz, tmy, tmo, tml;
     if (!make_tmap_3d_bf16(&tmz, p.z, p.dv, p.T, BH, 64, kStep) || !make_tmap_3d_bf16(&tmy, p.y, p.dqk, p.T, BH, 64, kStep) ||
         !(SEQ ? make_tmap_3d_bf16(&tmo, p.states, p.dqk, p.dv, BH * p.nseg, 64, 128)
               : make_tmap_3d_f32(&tmo, p.sums, p.dqk, p.dv, BH * p.nseg, 128)))
         return cudaErrorInvalidValue;
+    if (SEQ && p.last) {
+        if (!make_tmap_3d_f32(&tml, p.last, p.dqk, p.dv, BH, 128)) return cudaErrorInvalidValue;
+    } else {
+        tml = tmo;      // not used
+    }
     auto *const kernel = state_tc_kernel<NX, SEQ>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
     if (e != cudaSuccess) return e;
@@ -963,7 +983,7 @@ cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
     const size_t items = BH * zt * yt * (SEQ ? 1 : p.nseg);
     const unsigned grid = items < (size_t)sm_count() ? (unsigned)items : (unsigned)sm_count();
     const StatePlan pl{(int)items, fast_div(yt), fast_div(zt), fast_div(p.nseg), fast_div(p.H)};
-    kernel<<<grid, kStateThreads, C::BYTES, s>>>(tmz, tmy, tmo, p, pl, status);
+    kernel<<<grid, kStateThreads, C::BYTES, s>>>(tmz, tmy, tmo, tml, p, pl, status);
     return cudaGetLastError();
 }
 
