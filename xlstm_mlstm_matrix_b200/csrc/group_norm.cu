@@ -418,8 +418,12 @@ int tokens_per_block(int tokens, int G, int D, long long target) {
     const long long per = ((long long)tokens * G + target - 1) / target;
     return (int)((per + pass - 1) / pass * pass);
 }
-constexpr long long kFwdBlocks = 148 * 16;
-constexpr long long kBwdBlocks = 148 * 4;   // also bounds the partial sums
+// Forward: some blocks per SM more than the three that run at a time even out their ends (7B-like layer 139 us with 3 to
+// 8 per SM, 145 with 16, 167 with 64; D = 64: 59 us with 3, 47 with 8, 56 with 64).  Backward: the two that run at a
+// time, each with one partial sum (7B-like layer 262 us; 267 with 4, 286 with 16; 1001 x 5 fp32 groups of 80: 20.5 us,
+// 23.6, 27.6).
+constexpr long long kFwdBlocks = 148 * 8;
+constexpr long long kBwdBlocks = 148 * 2;   // also bounds the partial sums
 
 int bwd_chunks(const xlstm_group_norm_desc_t *d) {
     const int tokens = d->B * d->T, tpb = tokens_per_block(tokens, d->G, d->D, kBwdBlocks);
