@@ -30,6 +30,7 @@ LinStateP state_job(const LinAttnArgs &a, const Plan &pl, bool rev, char *ws) {
     p.y = rev ? a.q : a.k;
     p.init = rev ? a.dC1 : a.C0;
     p.last = rev ? a.dC0 : a.C1;
+    p.parts = 3;
     p.sums = reinterpret_cast<float *>(ws);
     p.states = a.dtype == XLSTM_BF16 ? ws + pl.sums : ws;
     return p;
@@ -91,7 +92,8 @@ cudaError_t launch_linattn_fwd(const LinAttnArgs &a, cudaStream_t s) {
 cudaError_t launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t s) {
     const Plan pl = plan(a);
     char *ws = static_cast<char *>(a.workspace);
-    const LinStateP p[2] = {state_job(a, pl, false, ws), state_job(a, pl, true, ws + pl.sums + pl.states)};
+    LinStateP p[2] = {state_job(a, pl, false, ws), state_job(a, pl, true, ws + pl.sums + pl.states)};
+    p[0].parts = 2;     // its final state is not an output
     const cudaError_t e = run_states(a, p, 2, s);
     if (e != cudaSuccess) return e;
     LinTiles t{};

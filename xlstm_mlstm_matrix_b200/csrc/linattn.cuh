@@ -55,6 +55,11 @@ struct LinStateP {
     float *sums;                 // U_n [B*H][nseg][dv*dqk]
     void *states;                // state entering each segment [B*H][nseg][dv*dqk]
     float *last;                 // state the chain ends in, or null
+    // bf16 parts of a weighted row w z.  Three are the fp32 product exactly: for chains whose end can leave in fp32.  Two
+    // leave less than 2^-15 of each term, for entering states alone, which are rounded to 2^-9 anyway (the 7B-like layer's
+    // backward, 4096 tokens: 170 us instead of 200).  By the call, not by `last`: an output's bits do not depend on whether
+    // the final state is asked for.
+    int parts;
 };
 // One output: out_t = scale sum_s l^{|t-s|} (x_t.y_s) z_s (s on t's past or future side) + rho_t (state of t's segment) x_t.
 struct LinTileP {

@@ -330,14 +330,15 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
     }
 }
 
-// Blocks hold 64 rows x 64 N columns.  Wide blocks read their rows fewer times, as long as a block per SM remains;
-// where not even one block of 64 x 64 per SM would run, a block holds 16 rows (a quarter of the work of each step
-// and four times the blocks).
+// Blocks hold 64 rows x 64 N columns.  Wide blocks read their rows fewer times, as long as a block per SM remains (whole
+// calls, T = 512, 256 x 256 with 16 heads: 132 us, 163 with 64 x 64 alone); where blocks of 64 x 64 would leave half the
+// SMs idle, a block holds 16 rows, a quarter of the work of each step and four times the blocks (T = 512, 64 x 64 with 2,
+// 8 and 16 heads: 21.5, 27.6 and 41.7 us, against 27.8, 29.7 and 29.7).
 struct Shape {
     int M, N;
 };
 Shape shape(int d, size_t blocks) {
-    if (blocks <= 148) return {1, 1};
+    if (blocks <= 74) return {1, 1};
     int n = d > 128 ? 4 : d > 64 ? 2 : 1;
     while (n > 1 && blocks / n < 148) n /= 2;
     return {4, n};

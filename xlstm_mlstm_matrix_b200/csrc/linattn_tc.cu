@@ -4,8 +4,8 @@
 // issued as tcgen05.mma by one thread, accumulated in tensor memory in fp32.
 //
 // state_tc_kernel: U_n = sum_s w_s z_s y_s^T, 128 z rows x NX y columns per block, 32 tokens a stage, chained over
-//   the segments where there are blocks enough.  The weighted rows w_s z_s enter as bf16 parts, two where only entering
-//   states are wanted, three where the chain's end leaves in fp32 (state_parts).
+//   the segments where there are blocks enough.  The weighted rows w_s z_s enter as two or three bf16
+//   parts (LinStateP::parts).
 // tile_tc_kernel: 128 tokens x NZ output columns per tile.  The tile's own rows X stay in shared memory; Y, Z and the
 //   entering state pass through a ring of 16 KB units.  Per 128 tokens of the segment the scores X Y^T land in tensor
 //   memory, are weighted with powers of the decay and written back as one bf16 copy (each rounding is relative to its
@@ -77,10 +77,6 @@ constexpr int kFold = 384;               // first thread of the fold warps
 // fold warps' (128 of them with NX = 256).
 constexpr int kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
 static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * 96, "no more than the launch brought");
-
-// Parts of the weighted rows.  Two leave 2^-16 of each term at most, far below the 2^-9 that an entering state is rounded to
-// anyway; three are the fp32 product exactly, for a final state that leaves in fp32.
-__device__ __forceinline__ int state_parts(const LinStateP &p) { return p.last ? 3 : 2; }
 
 // One tile's walk over its segments, the same in every role.
 struct StatePlan {
@@ -211,7 +207,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             // The whole warp walks the work, so that descriptors stay uniform; one lane issues.
             constexpr uint32_t id_u = make_idesc(128, NX, kFmtBF16, kFmtBF16, 1, 1);
             const bool leader = elect_one();
-            const int nq = state_parts(p);
+            const int nq = p.parts;
             const auto run = [&]() {
                 RingAt at, part;
                 int g = 0;          // segments summed
@@ -254,7 +250,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     } else if (warp < 12) {
         // ===================== weights =====================
         // the two groups take every other stage
-        const int t128 = tid & 127, group = (warp - 4) >> 2, nq = state_parts(p);
+        const int t128 = tid & 127, group = (warp - 4) >> 2, nq = p.parts;
         const int row = t128 / 8;       // of a stage; the thread's 16-byte chunks are in rows row and row + 16
         int c = 0, st = group, pp = group, phase = 0;      // stages so far; places of this group's next one and its parity
         bool go = true;
@@ -994,8 +990,10 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     // 224 KB: X twice where that leaves four slots for the ring, NZ / 64 boxes for the output, slots of two boxes
     const int slot_units = nkx > 1 || NZ > 64 ? 2 : 1, nx = nkx <= 2 ? 2 : 1;
     const int room = (14 - nx * nkx - NZ / 64) / slot_units, stages = room < kMaxRing ? room : kMaxRing;
-    // an item holds all z tiles of its tokens (X is read once) unless that leaves SMs without one
-    const int sms = sm_count(), zgroup = BH * tt >= 2ull * sms ? zt : 1;
+    // an item holds all z tiles of its tokens (X is read and weighted once) unless that leaves a quarter of the SMs without
+    // one: whole calls, T = 4096, 128 x 512 with 4 and 64 heads 47.1 and 279 us (one z tile per item: 51.2 and 354), with
+    // 2 heads 39.7 (36.9)
+    const int sms = sm_count(), zgroup = 4 * BH * tt >= 3ull * sms ? zt : 1;
     const int items = (int)(BH * tt * ((zt + zgroup - 1) / zgroup)), grid = items < sms ? items : sms;
     CUtensorMap tmx, tmy, tmz, tms, tmo;
     const bool ok =
@@ -1017,9 +1015,14 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
 
 }  // namespace
 
+// One block carries a tile through all segments (SEQ), unless few tiles leave most SMs idle while the segments are many.
+// Whole forward calls, T = 16384, d_qk x d_v 128 x 128 with 8, 64, 80 and 148 heads (one tile each): 279, 457, 510 and
+// 797 us, against 80, 424, 522 and 1000 us by single segments; 256 x 256 with 16 and 32 heads (two tiles each): 442 and
+// 552 against 328 and 620 us; T = 512 (two segments), 64 x 64 with 32 heads: 28.6 against 30.6 us.
 bool linattn_states_seq(const LinStateP &p) {
     const int nx = p.dqk > 128 ? 256 : p.dqk > 64 ? 128 : 64;
-    return p.nseg == 1 || (size_t)p.B * p.H * ((p.dv + 127) / 128) * ((p.dqk + nx - 1) / nx) >= 96;
+    const size_t tiles = (size_t)p.B * p.H * ((p.dv + 127) / 128) * ((p.dqk + nx - 1) / nx);
+    return p.nseg <= 2 || tiles >= (nx == 256 ? 56 : 72);
 }
 cudaError_t linattn_states_tc(const LinStateP &p, int32_t *status, cudaStream_t s) {
     if (linattn_states_seq(p))
