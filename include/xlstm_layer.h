@@ -29,6 +29,10 @@
  * With lens, tokens at or past lens[b] take no part, whatever q, k, v hold there (NaN
  * included); their rows of o, dq, dk and dv are written as zeros, and the final state is
  * the one after token lens[b] - 1.
+ * An infinity or NaN in a live token spreads to every later token (gradients: every
+ * earlier one) of its sequence and head, as in the recurrence, and, because segments are
+ * formed as masked products, it may reach the other tokens of its segment too (64 tokens
+ * fp32, 256 bf16).  Other sequences and heads keep their values.
  *
  * log_decay and lens need 4-byte alignment, every other pointer 16-byte alignment.
  */

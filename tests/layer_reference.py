@@ -83,19 +83,20 @@ def output_bound(ref, mag, T, d, dtype):
 
     fp32 inputs: roundings of half a step 2^-24 each, on the sum of magnitudes.
     bf16 inputs: the weighted scores and the entering state are one bf16 copy each (half a step 2^-8 of the part they
-    make), the state's own terms are bf16 pairs (2^-16), the sums fp32 (2^-23 a step), and the result is rounded once
-    (2^-8 of itself, plus the part of its error)."""
+    make), the state's own terms are pairs of bf16 values, the sums fp32 (2^-23 a step), and the result is rounded once
+    (2^-8 of itself, plus the part of its error).  A pair is cut off, not rounded: of the 24 significant bits the first
+    value holds the top 8 and the second 8 of the other 16 or better, which leaves less than 2^8 units of 2^-23 times
+    the term's power of two, 2^-15 of the term."""
     if dtype == torch.float32:
         return sum_roundings(T, d) * 2.0 ** -24 * mag
-    before = (2.0 ** -8 + 2.0 ** -16 + sum_roundings(T, d) * 2.0 ** -23) * mag
+    before = (2.0 ** -8 + 2.0 ** -15 + sum_roundings(T, d) * 2.0 ** -23) * mag
     return before + 2.0 ** -8 * (ref.abs() + before)
 
 
 def state_bound(mag, T, d, dtype):
-    """Bound on the fp32 final state (and its gradient): bf16 inputs enter as pairs, whose second rounding leaves
-    2^-16 of a term."""
-    u = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -23
-    return (sum_roundings(T, d) * u + (0.0 if dtype == torch.float32 else 2.0 ** -16)) * mag
+    """Bound on the fp32 final state (and its gradient): bf16 inputs enter as three bf16 values, which hold an fp32
+    product's 24 bits exactly."""
+    return sum_roundings(T, d) * (2.0 ** -24 if dtype == torch.float32 else 2.0 ** -23) * mag
 
 
 # ---- group norm ---------------------------------------------------------------------------------------------

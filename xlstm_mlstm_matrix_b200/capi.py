@@ -506,6 +506,18 @@ def _run(fn, index, stream, *args):
         raise XlstmError(st, fn.__name__)
 
 
+def _used_on(stream, index, *tensors):
+    """Tensors allocated by a helper (on the current stream) and used on `stream`: their memory is not given out again
+    before the work there is done."""
+    if stream is None:
+        return
+    if isinstance(stream, int):
+        stream = _torch.cuda.ExternalStream(stream, device=index)
+    for x in tensors:
+        if x is not None:
+            x.record_stream(stream)
+
+
 @functools.lru_cache(maxsize=256)
 def _linattn_plan(q_shape, dv, dtype, scale):
     """The descriptor of a shape, its forward and backward workspace sizes, and the shapes of v and of the state."""
@@ -543,6 +555,7 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
     torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 4)
     if out is None:
         o, C = torch.empty_like(v), torch.empty(plan[4], device=v.device, dtype=torch.float32)
+        _used_on(stream, index, o, C)
     else:
         o, C = out
         _want(o, "out[0]", plan[3], v.dtype, index)
@@ -550,6 +563,7 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
             _want(C, "out[1]", plan[4], torch.float32, index)
     if workspace is None:
         workspace = torch.empty(plan[1], device=v.device, dtype=torch.uint8)
+        _used_on(stream, index, workspace)
     _run(load().xlstm_linattn_fwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), o.data_ptr(), _raw(C), workspace.data_ptr(), workspace.numel())
     return o, C
@@ -561,6 +575,7 @@ def linattn_step(q, k, v, log_decay, state, scale=None, stream=None, out=None, i
     torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, None, scale, 3)
     if out is None:
         o, C = torch.empty_like(v), state if inplace else torch.empty_like(state)
+        _used_on(stream, index, o, None if inplace else C)
     else:
         o, C = out[0], state if inplace else out[1]
         _want(o, "out[0]", plan[3], v.dtype, index)
@@ -579,8 +594,10 @@ def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lens=None, scal
         _want(dstate, "dstate", plan[4], torch.float32, index)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dC0 = torch.empty(plan[4], device=v.device, dtype=torch.float32)
+    _used_on(stream, index, dq, dk, dv, dC0)
     if workspace is None:
         workspace = torch.empty(plan[2], device=v.device, dtype=torch.uint8)
+        _used_on(stream, index, workspace)
     _run(load().xlstm_linattn_bwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), do.data_ptr(), _raw(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
          dC0.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -633,6 +650,7 @@ def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads",
     torch, index, plan = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
     if out is None:
         out = torch.empty(plan[2], device=x.device, dtype=dt)
+        _used_on(stream, index, out)
     else:
         _want(out, "out", plan[2], dt, index)
     _run(load().xlstm_group_norm, index, stream, plan[0], x.data_ptr(), _raw(weight), _raw(bias), _raw(gate), out.data_ptr())
@@ -646,8 +664,10 @@ def group_norm_bwd(dy, x, weight=None, bias=None, gate=None, act="silu", layout=
     torch, index, plan = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dy.dtype)
     _want(dy, "dy", plan[2], dy.dtype, index)
     dx, dgate, dw, db = torch.empty_like(x), *(None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
+    _used_on(stream, index, dx, dgate, dw, db)
     if workspace is None and (weight is not None or bias is not None):
         workspace = torch.empty(plan[1], device=x.device, dtype=torch.uint8)
+        _used_on(stream, index, workspace)
     _run(load().xlstm_group_norm_bwd, index, stream, plan[0], x.data_ptr(), _raw(weight), _raw(bias), _raw(gate),
          dy.data_ptr(), dx.data_ptr(), _raw(dgate), _raw(dw), _raw(db), _raw(workspace),
          0 if workspace is None else workspace.numel())
