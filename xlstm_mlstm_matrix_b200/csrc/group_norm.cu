@@ -15,6 +15,7 @@
 #include "arg_checks.cuh"
 #include "common.cuh"
 #include "fast_div.cuh"
+#include "launch.cuh"
 #include "../../include/xlstm_layer.h"
 
 namespace xlstm {
@@ -185,6 +186,7 @@ __device__ __forceinline__ float normalise(const GroupNormP &p, const bool (&in)
 // layer's 805 MB).
 template <typename Tx, typename Ty, int LPR, int NV>
 __global__ void __launch_bounds__(kThreads, 3) group_norm_kernel(const GroupNormP p) {
+    wait_for_stream();
     using Q = Pipe<Tx, Ty, NV, 1>;
     constexpr int RPW = 32 / LPR, C = LPR * NV * kV;   // rows per warp, channels covered
     extern __shared__ uint4 stages[];
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 3) group_norm_kernel(const GroupNorm
 
 template <typename Tx, typename Ty, int LPR, int NV>
 __global__ void __launch_bounds__(kThreads, 2) group_norm_bwd_kernel(const GroupNormP p) {
+    wait_for_stream();
     using Q = Pipe<Tx, Ty, NV, 2>;
     constexpr int RPW = 32 / LPR, C = LPR * NV * kV;
     extern __shared__ uint4 stages[];
@@ -390,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_norm_bwd_kernel(const Group
 // dweight and dbias: the blocks' partial sums, eight interleaved runs per channel, added in a fixed order.
 __global__ void __launch_bounds__(kThreads) group_norm_sums_kernel(const float *part_w, const float *part_b, float *dw,
                                                                    float *db, int chunks, int C) {
+    wait_for_stream();
     __shared__ float red[kWarps][32];
     const float *part = blockIdx.y ? part_b : part_w;
     float *out = blockIdx.y ? db : dw;
@@ -433,11 +437,10 @@ int bwd_chunks(const xlstm_group_norm_desc_t *d) {
 template <typename Tx, typename Ty, int LPR, int NV, bool kBwd>
 cudaError_t launch(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
     constexpr int smem = Pipe<Tx, Ty, NV, kBwd ? 2 : 1>::BYTES;
-    void (*const kernel)(GroupNormP) = kBwd ? group_norm_bwd_kernel<Tx, Ty, LPR, NV> : group_norm_kernel<Tx, Ty, LPR, NV>;
+    void (*const kernel)(const GroupNormP) = kBwd ? group_norm_bwd_kernel<Tx, Ty, LPR, NV> : group_norm_kernel<Tx, Ty, LPR, NV>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(kernel, blocks, kThreads, smem, s, p);
 }
 template <typename Tx, typename Ty, bool kBwd>
 cudaError_t launch_types(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
@@ -545,9 +548,9 @@ xlstm_status_t xlstm_group_norm_bwd(const xlstm_group_norm_desc_t *desc, const v
     p.part_b = dbias ? ws + (size_t)chunks * C : nullptr;
     if (launch_any<true>(desc, p, stream) != cudaSuccess) return XLSTM_ERR_CUDA;
     if (sums) {
-        group_norm_sums_kernel<<<dim3((unsigned)((C + 31) / 32), 2), kThreads, 0, stream>>>(p.part_w, p.part_b, dweight,
-                                                                                            dbias, chunks, (int)C);
-        if (cudaGetLastError() != cudaSuccess) return XLSTM_ERR_CUDA;
+        if (launch_early(group_norm_sums_kernel, dim3((unsigned)((C + 31) / 32), 2), kThreads, 0, stream, p.part_w, p.part_b, dweight,
+                         dbias, chunks, (int)C) != cudaSuccess)
+            return XLSTM_ERR_CUDA;
     }
     return XLSTM_OK;
 }

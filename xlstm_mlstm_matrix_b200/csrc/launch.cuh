@@ -1,0 +1,35 @@
+// Launches whose start overlaps the end of the kernel before them on the stream.
+//
+// A call of several short kernels spends a good part of its time between them.  A kernel launched by launch_early may be
+// given to the SMs once every block of the kernel before has started (and said so) or ended, and waits on the device, before it
+// touches memory, until that kernel is complete.  As every kernel launched so waits, whatever ran earlier on the stream is
+// complete too.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace xlstm {
+
+// In every kernel that launch_early launches, before its first access to global memory, by all threads.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const Args &...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();     // reported here, not left for the next check
+    return e;
+}
+
+}  // namespace xlstm

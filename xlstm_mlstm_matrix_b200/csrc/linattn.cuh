@@ -16,6 +16,7 @@
 // Every power of l has an exponent >= 0, so no factor exceeds 1 whatever the decay.
 #pragma once
 #include "common.cuh"
+#include "launch.cuh"
 #include "../../include/xlstm_layer.h"
 
 namespace xlstm {

@@ -107,6 +107,7 @@ __device__ __forceinline__ void product_nn(float (&acc)[N][M][4], const float *a
 // ---- U_n = sum_s w_s z_s y_s^T of one segment, 16 M z rows x 64 N y columns per block ------------------
 template <int M, int N>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ LinStates jobs) {
+    wait_for_stream();
     extern __shared__ __align__(16) float sm[];
     constexpr int R = 16 * M;
     float *Zs = sm, *Ys = Zs + kSeg * R;      // [token][R], [token][64 N]
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
 // thousand segments one rounded factor would drift the oldest tokens' weight by a thousand of its roundings.
 template <typename S>
 __global__ void __launch_bounds__(kChain) chain_kernel(const __grid_constant__ LinStates jobs) {
+    wait_for_stream();
     unsigned id;
     const LinStateP &p = jobs.p[job_of_block(jobs, id)];
     const size_t area = (size_t)p.dv * p.dqk;
@@ -227,6 +229,7 @@ struct TileSmem {
 };
 template <int M, int N>
 __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __grid_constant__ LinTiles jobs, int32_t *status) {
+    wait_for_stream();
     using S = TileSmem<N>;
     extern __shared__ __align__(16) float sm[];
     float *Ps = sm + S::STEPS * S::STEP;       // weighted scores, two tiles of kK tokens
@@ -360,8 +363,7 @@ cudaError_t tile_mn(LinTiles &jobs, int32_t *status, cudaStream_t s) {
     });
     const cudaError_t e = cudaFuncSetAttribute(tile_kernel<M, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tile_kernel<M, N><<<blocks, kThreads, smem, s>>>(jobs, status);
-    return cudaGetLastError();
+    return launch_early(tile_kernel<M, N>, blocks, kThreads, smem, s, jobs, status);
 }
 template <int M, int N>
 cudaError_t sums_mn(LinStates &jobs, cudaStream_t s) {
@@ -371,8 +373,7 @@ cudaError_t sums_mn(LinStates &jobs, cudaStream_t s) {
     });
     const cudaError_t e = cudaFuncSetAttribute(sums_kernel<M, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    sums_kernel<M, N><<<blocks, kThreads, smem, s>>>(jobs);
-    return cudaGetLastError();
+    return launch_early(sums_kernel<M, N>, blocks, kThreads, smem, s, jobs);
 }
 
 }  // namespace
@@ -402,9 +403,7 @@ cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s) {
     const unsigned blocks = number_blocks(jobs, [](const LinStateP &p) {
         return (size_t)p.B * p.H * (((size_t)p.dv * p.dqk / 4 + kChain - 1) / kChain);
     });
-    if (bf16) chain_kernel<__nv_bfloat16><<<blocks, kChain, 0, s>>>(jobs);
-    else chain_kernel<float><<<blocks, kChain, 0, s>>>(jobs);
-    return cudaGetLastError();
+    return launch_early(bf16 ? chain_kernel<__nv_bfloat16> : chain_kernel<float>, blocks, kChain, 0, s, jobs);
 }
 
 }  // namespace xlstm

@@ -25,7 +25,8 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bf
 
 // NC: float4 columns per lane and row.
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepP p) {
+__global__ void __launch_bounds__(kThreads) linattn_step_kernel(const __grid_constant__ StepP p) {
+    wait_for_stream();
     const int G = p.dqk >> 2;                                        // float4s of a row
     const int LG = (G <= 32 && (G & (G - 1)) == 0) ? G : 32;         // lanes per row
     const int RW = 32 / LG;                                          // rows per warp and pass
@@ -103,13 +104,9 @@ cudaError_t launch_linattn_step(const LinAttnArgs &a, cudaStream_t s) {
     const dim3 grid((unsigned)BH, split);
     const int G = a.dqk / 4, LG = (G <= 32 && (G & (G - 1)) == 0) ? G : 32, nc = (G + LG - 1) / LG;
 #define LINATTN_STEP(NCV)                                                            \
-    if (nc == NCV) {                                                                 \
-        if (a.dtype == XLSTM_BF16)                                                   \
-            linattn_step_kernel<__nv_bfloat16, NCV><<<grid, kThreads, 0, s>>>(p);    \
-        else                                                                         \
-            linattn_step_kernel<float, NCV><<<grid, kThreads, 0, s>>>(p);            \
-        return cudaGetLastError();                                                   \
-    }
+    if (nc == NCV)                                                                                             \
+        return launch_early(a.dtype == XLSTM_BF16 ? linattn_step_kernel<__nv_bfloat16, NCV>                    \
+                                                  : linattn_step_kernel<float, NCV>, grid, kThreads, 0, s, p);
     LINATTN_STEP(1) LINATTN_STEP(2) LINATTN_STEP(3) LINATTN_STEP(4)
 #undef LINATTN_STEP
     return cudaErrorInvalidValue;

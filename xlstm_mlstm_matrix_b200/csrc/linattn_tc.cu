@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tmem_slot;
+    wait_for_stream();
 
     if (warp < 4) set_registers<kIoRegs, false>();
     else if (warp < 12) set_registers<kWeightRegs, false>();
@@ -574,6 +575,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tmem_slot;
+    wait_for_stream();
     const auto scores_at = [&](int k) { return tm + 256 + 128 * (k & 1); };
     const auto acc_at = [&](int i) { return tm + 128 * (i & 1); };
     TileItem w;
@@ -979,8 +981,7 @@ cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
     const size_t items = BH * zt * yt * (SEQ ? 1 : p.nseg);
     const unsigned grid = items < (size_t)sm_count() ? (unsigned)items : (unsigned)sm_count();
     const StatePlan pl{(int)items, fast_div(yt), fast_div(zt), fast_div(p.nseg), fast_div(p.H)};
-    kernel<<<grid, kStateThreads, C::BYTES, s>>>(tmz, tmy, tmo, tml, p, pl, status);
-    return cudaGetLastError();
+    return launch_early(kernel, grid, kStateThreads, C::BYTES, s, tmz, tmy, tmo, tml, p, pl, status);
 }
 
 template <int NZ>
@@ -1009,8 +1010,7 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     while ((1 << seg_shift) < p.G) ++seg_shift;
     const TilePlan pl{items, zgroup, zt, nkx, nx, stages, slot_units * kUnit, seg_shift,
                       fast_div((zt + zgroup - 1) / zgroup), fast_div(tt), fast_div(p.H)};
-    tile_tc_kernel<NZ><<<grid, kTileThreads, smem, s>>>(tmx, tmy, tmz, tms, tmo, p, pl, status);
-    return cudaGetLastError();
+    return launch_early(tile_tc_kernel<NZ>, grid, kTileThreads, smem, s, tmx, tmy, tmz, tms, tmo, p, pl, status);
 }
 
 }  // namespace
