@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // against Z; both walk the work as whole warps, so that operands stay in uniform registers (issued from a single-thread
 // branch a product took 110 to 170 cycles, not 64).
 constexpr int kTab = 32 + 132 + 32;     // powers of the decay, room for masked columns on both sides
-constexpr int kTileThreads = 640;       // TMA, two of products, one idle; eight warps of weights; eight of scaling and read-out
+constexpr int kTileThreads = 640;       // TMA, two of products, one of zeros; eight warps of weights; eight of scaling and read-out
 constexpr int kMaxRing = 10;
 struct TileBars {                       // indices into the barrier array; pairs are one per buffer
     static constexpr int XFULL = 0, XFREE = 2, SCORES = 4, WEIGHTS = 6, PRODUCT = 8, ENTRY = 10, SCALED = 12, DONE = 14,
@@ -474,53 +474,70 @@ struct TileBars {                       // indices into the barrier array; pairs
 };
 constexpr int kTileTail = 2 * kTab * 4 + (TileBars::RING + 2 * kMaxRing) * 8 + 16;
 
-// What a block has to know of one item: 128 tokens of a head, with the z tiles z .. z_end of its output.
+// One item: 128 tokens of a head, with the z tiles z .. z_end of its output.
 struct TileItem {
     int bh, t0, len, n, s0, e, nj, z, z_end;
     float ld;                          // the head's log decay
-    bool entry, live, more;      // live: with tokens; more: there is an item
+    bool entry;
 };
-// The items of a block: rounds over the grid, turned by 37 blocks each so that a block meets every place within the
-// segments (whose tiles have between one and G / 128 units).
 struct TilePlan {
     int items, zgroup, ztiles, nkx, nx, stages, slot_bytes, seg_shift;     // segments of 2^seg_shift tokens
-    FastDiv by_zgroups, by_ttiles, by_H;
+    FastDiv by_zgroups, by_ttiles, by_H, by_grid;
 };
+// The items of a block, the same in every role: rounds over the grid, turned by 37 blocks each so that a block meets every
+// place within the segments (whose tiles have between one and G / 128 units).  A warp looks 32 rounds up at a time, a round
+// per lane, and hands the lanes' items out: looked up one by one, the lengths' and decays' latency was most of the time of
+// short items (4096 items without a live token: 49 us, now 13).
 struct TileWalk {
-    int round, turn;
-    __device__ __forceinline__ TileWalk() : round(0), turn(blockIdx.x) {}
+    int next;                          // round of the next look-up
+    unsigned mask;                     // lanes whose item is still to come
+    int bh, t0, len, zg;               // this lane's item
+    float ld;
+    __device__ __forceinline__ TileWalk() : next(0), mask(0) {}
 };
-// The next item of the walk.  Not inlined: in every role's loop it would take a fifth of the kernel's code, and
-// instruction fetch is what the warps of this kernel wait for most.
-__device__ __noinline__ TileItem next_item(const LinTileP &p, const TilePlan &pl, TileWalk &walk) {
-    TileItem w;
-    w.live = false;
-    for (;;) {
-        int id = walk.round + walk.turn;
-        w.more = walk.round < pl.items;
-        if (!w.more) return w;
-        walk.round += gridDim.x;
-        walk.turn += 37;
-        while (walk.turn >= (int)gridDim.x) walk.turn -= gridDim.x;
-        if (id >= pl.items) continue;     // the last round's idle blocks
-        int zg = id, t = quotient(id, pl.by_zgroups);
-        zg -= t * (int)pl.by_zgroups.d;
-        w.bh = split(t, pl.by_ttiles);
-        w.z = zg * pl.zgroup;
-        w.z_end = min(w.z + pl.zgroup, pl.ztiles);
-        w.t0 = t * 128;
-        const int b = quotient(w.bh, pl.by_H);
-        w.len = seq_len(p.lens, b, p.T);
-        w.n = w.t0 >> pl.seg_shift;
-        w.s0 = w.n << pl.seg_shift;
-        w.e = min(w.s0 + p.G, w.len);
-        w.entry = p.rev ? (w.e < w.len || p.has_init) : (w.n > 0 || p.has_init);
-        // 128-token score tiles on this tile's past (future) side, its own first
-        w.nj = p.rev ? (w.e - w.t0 + 127) / 128 : (w.t0 - w.s0) / 128 + 1;
-        w.ld = head_log_decay(p.log_decay, w.bh - b * p.H);
-        w.live = w.t0 < w.len;
-        return w;
+// Not inlined: in every role's loop it would take a fifth of the kernel's code, which the warps of this kernel wait for often.
+template <bool LIVE>
+__device__ __noinline__ TileWalk look_up(const LinTileP &p, const TilePlan &pl, int first) {
+    TileWalk k;
+    const int round = first + (threadIdx.x & 31), grid = gridDim.x;
+    k.next = first + 32;
+    int turn = blockIdx.x + 37 * round;
+    turn -= quotient(turn, pl.by_grid) * grid;
+    const int id = round * grid + turn;
+    const bool is = id < pl.items;      // (not in the last round's idle blocks)
+    k.zg = is ? id : 0;
+    int t = quotient(k.zg, pl.by_zgroups);
+    k.zg -= t * (int)pl.by_zgroups.d;
+    k.bh = split(t, pl.by_ttiles);
+    k.t0 = t * 128;
+    const int b = quotient(k.bh, pl.by_H);
+    k.len = seq_len(p.lens, b, p.T);
+    k.ld = head_log_decay(p.log_decay, k.bh - b * p.H);
+    k.mask = __ballot_sync(0xffffffffu, is && (k.t0 < k.len) == LIVE);
+    return k;
+}
+// The next item with (LIVE) or without tokens of its sequence; false behind the last.  Warp-wide.
+template <bool LIVE>
+__device__ __forceinline__ bool next_item(const LinTileP &p, const TilePlan &pl, TileWalk &k, TileItem &w) {
+    while (!k.mask) {
+        if (k.next * (int)gridDim.x >= pl.items) return false;
+        k = look_up<LIVE>(p, pl, k.next);
     }
+    const int from = __ffs(k.mask) - 1;
+    k.mask &= k.mask - 1;
+    w.bh = __shfl_sync(0xffffffffu, k.bh, from);
+    w.t0 = __shfl_sync(0xffffffffu, k.t0, from);
+    w.len = __shfl_sync(0xffffffffu, k.len, from);
+    w.z = __shfl_sync(0xffffffffu, k.zg, from) * pl.zgroup;
+    w.ld = __shfl_sync(0xffffffffu, k.ld, from);
+    w.z_end = min(w.z + pl.zgroup, pl.ztiles);
+    w.n = w.t0 >> pl.seg_shift;
+    w.s0 = w.n << pl.seg_shift;
+    w.e = min(w.s0 + p.G, w.len);
+    w.entry = p.rev ? (w.e < w.len || p.has_init) : (w.n > 0 || p.has_init);
+    // 128-token score tiles on this tile's past (future) side, its own first
+    w.nj = p.rev ? (w.e - w.t0 + 127) / 128 : (w.t0 - w.s0) / 128 + 1;
+    return true;
 }
 
 template <int NZ>
@@ -592,8 +609,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 return ok;
             };
             TileWalk walk;
-            while ((w = next_item(p, pl, walk)).more) {
-                if (!w.live) continue;
+            while (next_item<true>(p, pl, walk, w)) {
                 const int xb = xi % nx;
                 if (xi >= nx && !waitw(sh, &bar[TileBars::XFREE + xb], (xi / nx - 1) & 1, kWhereTileX)) return;
                 if (lane == 0) {
@@ -673,8 +689,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             RingAt at;
             int xi = 0, k = 0, i = 0, zc = 0;           // items, units, tiles and slots of Z so far
             TileWalk walk;
-            while ((w = next_item(p, pl, walk)).more) {
-                if (!w.live) continue;
+            while (next_item<true>(p, pl, walk, w)) {
                 const int xb = nx == 2 ? xi & 1 : 0;
                 if (!waitw(sh, &bar[TileBars::XFULL + xb], (nx == 2 ? xi >> 1 : xi) & 1, kWhereTileX)) return;
                 const uint64_t x = smem_desc_sw128(smem_u32(sm + xb * nkx * kUnit), 16, 1024);
@@ -753,8 +768,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             RingAt at;
             int k0 = 0, i = 0, zc = 0;      // the item's first unit; tiles and slots of Z so far
             TileWalk walk;
-            for (; (w = next_item(p, pl, walk)).more; k0 += w.live ? w.nj : 0) {
-                if (!w.live) continue;
+            for (; next_item<true>(p, pl, walk, w); k0 += w.nj) {
                 for (int z = w.z; z < w.z_end; ++z, ++i)
                     for (int j = 0; j < w.nj; ++j, ++zc) {
                         const int k = k0 + j;
@@ -787,7 +801,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             drain_wait(&bar[TileBars::LAST + 1], 0);
         }
     } else if (warp == 3) {
-        // idle: the arithmetic warps start at a multiple of four
+        // ===================== tiles behind their sequence: zeros =====================
+        TileWalk walk;
+        while (next_item<false>(p, pl, walk, w)) {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)w.bh * p.T + w.t0) * p.dz;
+            const int c0 = w.z * NZ, c1 = min(w.z_end * NZ, p.dz), rows = min(128, p.T - w.t0);
+            for (int c = c0 + lane % 8 * 8; c < c1; c += 64) {
+                __nv_bfloat16 *at = o + (size_t)(lane / 8) * p.dz + c;
+#pragma unroll 8
+                for (int row = lane / 8; row < rows; row += 4, at += 4 * p.dz) *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+            }
+        }
     } else if (warp < 4 + kMath) {
         // ===================== weights =====================
         const int quarter = warp & 3, half = (warp - 4) >> 2, r = 32 * quarter + lane;
@@ -795,8 +819,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto run = [&]() {
             int k = 0, xi = 0;
             TileWalk walk;
-            while ((w = next_item(p, pl, walk)).more) {
-                if (!w.live) continue;
+            while (next_item<true>(p, pl, walk, w)) {
                 const float ld = w.ld;
                 // Column c of a score tile at distance d tiles carries l^(128 (d - 1)) times tab[c] times the row's power.
                 // A warp that writes this item's table has seen all warps write the one before, and so leave the one
@@ -878,16 +901,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto run = [&]() {
             int i = 0;
             TileWalk walk;
-            while ((w = next_item(p, pl, walk)).more) {
-                if (!w.live) {      // behind the sequence: zeros
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)w.bh * p.T + w.t0) * p.dz;
-                    const int c0 = w.z * NZ, width = (min(w.z_end * NZ, p.dz) - c0) / 8;
-                    for (int q = tid - 32 * (4 + kMath); q < 128 * width; q += 32 * kMath) {
-                        const int row = q / width, c = c0 + q % width * 8;
-                        if (w.t0 + row < p.T) *reinterpret_cast<uint4 *>(o + (size_t)row * p.dz + c) = make_uint4(0, 0, 0, 0);
-                    }
-                    continue;
-                }
+            while (next_item<true>(p, pl, walk, w)) {
                 const float ld = w.ld;
                 const int t = w.t0 + r;
                 const float rho = p.rev ? decay_pow(ld, max(w.e - 1 - t, 0)) : p.scale * decay_pow(ld, t - w.s0 + 1);
@@ -1009,7 +1023,7 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     int seg_shift = 7;
     while ((1 << seg_shift) < p.G) ++seg_shift;
     const TilePlan pl{items, zgroup, zt, nkx, nx, stages, slot_units * kUnit, seg_shift,
-                      fast_div((zt + zgroup - 1) / zgroup), fast_div(tt), fast_div(p.H)};
+                      fast_div((zt + zgroup - 1) / zgroup), fast_div(tt), fast_div(p.H), fast_div(grid)};
     return launch_early(tile_tc_kernel<NZ>, grid, kTileThreads, smem, s, tmx, tmy, tmz, tms, tmo, p, pl, status);
 }
 
