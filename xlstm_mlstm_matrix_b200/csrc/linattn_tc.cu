@@ -111,6 +111,9 @@ __device__ __forceinline__ StateWalk state_walk(const LinStateP &p, const StateP
     else w.nm = w.first < w.nseg && (p.last || w.first != (p.rev ? 0 : w.nseg - 1)) ? 1 : 0;
     return w;
 }
+// Boxes of 64 z rows that exist.  Without the second one its place is neither filled nor weighted: what lies there makes
+// rows of the state that are not stored.
+__device__ __forceinline__ int z_boxes(const LinStateP &p, const StateWalk &w) { return w.z0 + 64 < p.dv ? 2 : 1; }
 // The k-th segment in chain order.
 template <bool SEQ>
 __device__ __forceinline__ int segment_of(const LinStateP &p, const StateWalk &w, int k) {
@@ -167,6 +170,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             bool go = true;
             for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
                 const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
+                const int zboxes = z_boxes(p, w);
                 for (int k = 0; go && k < w.nm; ++k) {
                     const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
                     for (int t = s0; t < e; t += kStep, ++c) {
@@ -180,8 +184,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         const bool ends = p.lens && t + kStep > w.len;
                         uint64_t *landed = &bar[ends ? C::B_RAW : C::B_FULL + st];
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(landed, kPart + C::Y_BYTES);
-                            for (int b = 0; b < 2; ++b) tma_load_3d(Zs + 4096 * b, &tmz, landed, w.z0 + 64 * b, t, w.bh);
+                            mbar_arrive_expect_tx(landed, zboxes * (kPart / 2) + C::Y_BYTES);
+                            for (int b = 0; b < zboxes; ++b) tma_load_3d(Zs + 4096 * b, &tmz, landed, w.z0 + 64 * b, t, w.bh);
                             for (int b = 0; b < NX / 64; ++b) tma_load_3d(Ys + 4096 * b, &tmy, landed, w.y0 + 64 * b, t, w.bh);
                         }
                         if (ends) {
@@ -190,7 +194,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                                 break;
                             }
                             ++raw;
-                            for (int b = 0; b < 2 + NX / 64; ++b) zero_rows<kStep>(Zs + 4096 * b, w.len - t, lane);
+                            for (int b = 0; b < 2 + NX / 64; ++b)
+                                if (b < zboxes || b >= 2) zero_rows<kStep>(Zs + 4096 * b, w.len - t, lane);
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar[C::B_FULL + st]);
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         bool go = true;
         for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
             const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
+            const int chunks = 2 * z_boxes(p, w);
             const float ld = w.ld;
             // the weights of a stage: a power per stage times these (one rounding more than the power itself)
             const float own[2] = {p.rev ? p.scale * decay_pow(ld, row + 1) : decay_pow(ld, kStep - 1 - row),
@@ -285,7 +291,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     uint8_t *parts = sm + C::OFF_PARTS + pp * C::PARTS_BYTES;
                     uint4 u[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<uint4 *>(Zs + 16 * (t128 + 128 * i));
+                    for (int i = 0; i < 4; ++i)
+                        if (i < chunks) u[i] = *reinterpret_cast<uint4 *>(Zs + 16 * (t128 + 128 * i));
                     // the products of the stage PARTS ago have read the place of the parts
                     // (none before the first PARTS stages: a barrier's phase before its first counts as over)
                     const bool wrapped = st < C::PARTS;
@@ -295,6 +302,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        if (i >= chunks) break;
                         uint4 part[3];
                         split_scaled(u[i], wt[i & 1], part);
 #pragma unroll
