@@ -123,6 +123,19 @@ def test_padded_batch(dims, dtype):
     assert torch.equal(C[0], x["state"][0]) and torch.equal(g["dC0"][0], x["dstate"][0])
 
 
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("state", [False, True], ids=["zero", "state"])
+@pytest.mark.parametrize("shape", [(24, 3, 700, 64, 64), (9, 8, 600, 128, 96), (10, 6, 800, 256, 80), (7, 4, 780, 272, 160)], ids=str)
+def test_many_heads(shape, state, ragged):
+    """Heads enough for a block to carry a whole head's state, over more than two segments (bf16)."""
+    lens = None
+    if ragged:
+        lens = ([shape[2], 0, 1, 255, 256, 257, 512, 513, 599] + list(range(300, 320)))[:shape[0]]
+    x = make(*shape, BF16, seed=21, state=state, lens=lens)
+    check_fwd(x)
+    check_bwd(x)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("decay", [0.0, 0.5, -1e-7, -0.69, -30.0, -1e30, float("-inf")])
 def test_decays(decay, dtype):

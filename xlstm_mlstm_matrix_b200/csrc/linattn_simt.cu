@@ -403,7 +403,11 @@ cudaError_t linattn_chain(LinStates jobs, bool bf16, cudaStream_t s) {
     const unsigned blocks = number_blocks(jobs, [](const LinStateP &p) {
         return (size_t)p.B * p.H * (((size_t)p.dv * p.dqk / 4 + kChain - 1) / kChain);
     });
-    return launch_early(bf16 ? chain_kernel<__nv_bfloat16> : chain_kernel<float>, blocks, kChain, 0, s, jobs);
+    if (!bf16) return launch_early(chain_kernel<float>, blocks, kChain, 0, s, jobs);
+    // Not early: the kernel before holds the registers of all SMs, and the SMs that it leaves first would take most of the
+    // blocks (long context, 8 heads x 65536 tokens, whole call: 270 us, so 244).
+    chain_kernel<__nv_bfloat16><<<blocks, kChain, 0, s>>>(jobs);
+    return cudaGetLastError();
 }
 
 }  // namespace xlstm
