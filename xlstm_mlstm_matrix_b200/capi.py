@@ -476,7 +476,7 @@ def _load_torch():
 
 
 def _want(x, name, shape, dtype, index):
-    """x is a contiguous tensor of this shape and type on CUDA device `index`."""
+    """x is a contiguous tensor of this shape and type on CUDA device `index` (callers on hot paths test that first)."""
     if x.dtype == dtype and x.shape == shape and x.get_device() == index and x.is_contiguous():
         return
     if x.dtype != dtype:
@@ -522,7 +522,10 @@ def _used_on(stream, index, *tensors):
 def _linattn_plan(q_shape, dv, dtype, scale):
     """The descriptor of a shape, its forward and backward workspace sizes, and the shapes of v and of the state."""
     B, H, T, dqk = q_shape if len(q_shape) == 4 else (*q_shape[:2], 1, q_shape[2])
-    desc = make_linattn_desc(B, H, T, dqk, dv, dtype, dqk ** -0.5 if scale is None else float(scale))
+    code = {_torch.float32: XLSTM_F32, _torch.bfloat16: XLSTM_BF16}
+    if dtype not in code:
+        raise TypeError(f"q, k and v must be bf16 or fp32, got {dtype}")
+    desc = make_linattn_desc(B, H, T, dqk, dv, code[dtype], dqk ** -0.5 if scale is None else float(scale))
     return (desc, max(256, xlstm_linattn_workspace_size(desc)), max(256, xlstm_linattn_bwd_workspace_size(desc)),
             (*q_shape[:-1], dv), (B, H, dv, dqk), (B,), (H,))
 
@@ -532,10 +535,13 @@ def _linattn_inputs(q, k, v, log_decay, state, lens, scale, axes):
     dt, shape, index = q.dtype, q.shape, q.get_device()
     if len(shape) != axes or v.dim() != axes:
         raise ValueError(f"q: {q.dim()} axes, v: {v.dim()} axes, expected {axes}")
-    plan = _linattn_plan(shape, v.shape[-1], _dtype_code(q), scale)
-    _want(q, "q", shape, dt, index)
-    _want(k, "k", shape, dt, index)
-    _want(v, "v", plan[3], dt, index)
+    plan = _linattn_plan(shape, v.shape[-1], dt, scale)
+    if not q.is_contiguous():
+        _want(q, "q", shape, dt, index)
+    if k.dtype != dt or k.shape != shape or k.get_device() != index or not k.is_contiguous():
+        _want(k, "k", shape, dt, index)
+    if v.dtype != dt or v.shape != plan[3] or v.get_device() != index or not v.is_contiguous():
+        _want(v, "v", plan[3], dt, index)
     _want(log_decay, "log_decay", plan[6], torch.float32, index)
     if state is not None:
         _want(state, "state", plan[4], torch.float32, index)
@@ -554,7 +560,7 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
     out: (o, C) to write into; C may be None (not formed)."""
     torch, index, plan = _linattn_inputs(q, k, v, log_decay, state, lens, scale, 4)
     if out is None:
-        o, C = torch.empty_like(v), torch.empty(plan[4], device=v.device, dtype=torch.float32)
+        o, C = torch.empty_like(v), torch.empty_like(state) if state is not None else log_decay.new_empty(plan[4])
         _used_on(stream, index, o, C)
     else:
         o, C = out
@@ -562,7 +568,7 @@ def linattn_fwd(q, k, v, log_decay, state=None, lens=None, scale=None, stream=No
         if C is not None:
             _want(C, "out[1]", plan[4], torch.float32, index)
     if workspace is None:
-        workspace = torch.empty(plan[1], device=v.device, dtype=torch.uint8)
+        workspace = v.new_empty(plan[1], dtype=torch.uint8)
         _used_on(stream, index, workspace)
     _run(load().xlstm_linattn_fwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), o.data_ptr(), _raw(C), workspace.data_ptr(), workspace.numel())
@@ -593,10 +599,10 @@ def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lens=None, scal
     if dstate is not None:
         _want(dstate, "dstate", plan[4], torch.float32, index)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dC0 = torch.empty(plan[4], device=v.device, dtype=torch.float32)
+    dC0 = torch.empty_like(state) if state is not None else log_decay.new_empty(plan[4])
     _used_on(stream, index, dq, dk, dv, dC0)
     if workspace is None:
-        workspace = torch.empty(plan[2], device=v.device, dtype=torch.uint8)
+        workspace = v.new_empty(plan[2], dtype=torch.uint8)
         _used_on(stream, index, workspace)
     _run(load().xlstm_linattn_bwd, index, stream, plan[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          _raw(lens), _raw(state), do.data_ptr(), _raw(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
@@ -627,7 +633,8 @@ def _group_norm_inputs(x, weight, bias, gate, act, layout, eps, y_dtype):
     torch = _torch or _load_torch()
     index = x.get_device()
     plan = _group_norm_plan(x.shape, x.dtype, y_dtype, layout, act, eps)
-    _want(x, "x", x.shape, x.dtype, index)
+    if not x.is_contiguous():
+        _want(x, "x", x.shape, x.dtype, index)
     if weight is not None:
         _want(weight, "weight", plan[3], torch.float32, index)
     if bias is not None:
@@ -649,7 +656,7 @@ def group_norm(x, weight=None, bias=None, gate=None, act="silu", layout="heads",
     dt = out.dtype if out is not None else out_dtype if out_dtype is not None else gate.dtype if gate is not None else x.dtype
     torch, index, plan = _group_norm_inputs(x, weight, bias, gate, act, layout, eps, dt)
     if out is None:
-        out = torch.empty(plan[2], device=x.device, dtype=dt)
+        out = torch.empty_like(gate) if gate is not None else x.new_empty(plan[2], dtype=dt)
         _used_on(stream, index, out)
     else:
         _want(out, "out", plan[2], dt, index)
@@ -666,7 +673,7 @@ def group_norm_bwd(dy, x, weight=None, bias=None, gate=None, act="silu", layout=
     dx, dgate, dw, db = torch.empty_like(x), *(None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
     _used_on(stream, index, dx, dgate, dw, db)
     if workspace is None and (weight is not None or bias is not None):
-        workspace = torch.empty(plan[1], device=x.device, dtype=torch.uint8)
+        workspace = x.new_empty(plan[1], dtype=torch.uint8)
         _used_on(stream, index, workspace)
     _run(load().xlstm_group_norm_bwd, index, stream, plan[0], x.data_ptr(), _raw(weight), _raw(bias), _raw(gate),
          dy.data_ptr(), dx.data_ptr(), _raw(dgate), _raw(dw), _raw(db), _raw(workspace),
