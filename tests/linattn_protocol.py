@@ -81,15 +81,11 @@ def tile_protocol(items, nslots: int, stages: int, nx: int, relays: int = 4) -> 
                     P.arrive("products", f"PRODUCT{s}", k)
                 zc += 1
             P.arrive("products", f"DONE{b}", i)
-            # scaling and read-out: the storer frees the staging memory and stores from it
+            # scaling and read-out (each warp stores what it read)
             P.wait("read-out", f"ENTRY{b}", i)
             P.arrive("read-out", f"SCALED{b}", i)
             P.wait("read-out", f"DONE{b}", i)
-            P.arrive("read-out", "OUT_FREE", i)
-            P.wait("read-out", "OUT_FREE", i)
             P.arrive("read-out", f"TAKEN{b}", i)
-            P.arrive("read-out", "OUT_FULL", i)
-            P.wait("read-out", "OUT_FULL", i)
             i += 1
         k0 += units
     return P
@@ -99,15 +95,9 @@ def state_protocol(segments, stages: int, parts: int, accs: int, skip_last: bool
     """state_tc_kernel.  segments: per tile, the stages of each of its segments in chain order; skip_last: the last
     segment's sum is not formed.  Two groups of warps weight every other stage."""
     P = Protocol()
-    c = g = stores = 0
+    c = g = 0
     for tile in segments:
         for si, n in enumerate(tile):
-            if si:                      # the state entering this segment leaves through the staging memory
-                P.arrive("fold", "OUT_FREE", stores)
-                P.wait("fold", "OUT_FREE", stores)
-                P.arrive("fold", "OUT_FULL", stores)
-                P.wait("fold", "OUT_FULL", stores)
-                stores += 1
             if skip_last and si == len(tile) - 1:
                 continue
             if g >= accs:

@@ -19,10 +19,10 @@ namespace {
 
 // Codes of the bounded waits in the status block.
 enum : int {
-    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206, kWhereSumOut = 207, kWhereSumRaw = 208,
+    kWhereSumEmpty = 201, kWhereSumFull = 202, kWhereSumScaled = 203, kWhereSumDone = 204, kWhereSumTaken = 205, kWhereSumParts = 206, kWhereSumRaw = 208,
     kWhereTileEmpty = 211, kWhereTileX = 212, kWhereTileFull = 213, kWhereTileScores = 214, kWhereTileWeights = 215,
     kWhereTileEntry = 216, kWhereTileProduct = 217, kWhereTileDone = 218, kWhereTileTaken = 219, kWhereTileTable = 220,
-    kWhereTileOut = 221, kWhereTileRaw = 222,
+    kWhereTileRaw = 222,
 };
 
 constexpr int kMath = 8;            // warps of one arithmetic role
@@ -54,19 +54,17 @@ struct StateCfg {
     static constexpr int ACCS = 2;      // two sums take turns in tensor memory
     // A place holds a stage from the start of its loads (some 2000 cycles) through its weighting (as long) to the end of
     // its products (400 to 800).  The first part takes the place of z; the others have PARTS places of their own.
-    static constexpr int STAGES = NX == 256 || (!SEQ && NX == 128) ? 6 : 8, PARTS = STAGES / 2;
+    static constexpr int STAGES = NX == 256 ? 6 : 8, PARTS = STAGES / 2;
     static constexpr int Y_BYTES = NX * kStep * 2;
     static constexpr int STAGE = kPart + Y_BYTES;               // z and y as they come
     static constexpr int OFF_PARTS = STAGES * STAGE, PARTS_BYTES = 2 * kPart;
     static constexpr int OFF_OUT = OFF_PARTS + PARTS * PARTS_BYTES;
-    // What a store leaves from, boxes of 128 rows x 128 bytes.  SEQ: an entering state leaves in ROUNDS stores, the final
-    // one in NX / 64, of one box of each half.
-    static constexpr int ROUNDS = NX == 256 ? 2 : 1;
-    static constexpr int OUT = SEQ ? 32768 : 128 * NX * 4;
+    // 4 KB per fold warp, what one of its stores leaves from: 32 rows x 64 (32) columns bf16, or x 32 columns fp32.
+    static constexpr int OUT = 8 * 4096;
+    static constexpr int BF16_COLS = NX == 64 ? 32 : 64;
     static constexpr int OFF_BAR = OFF_OUT + OUT;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_SCALED = 2 * STAGES, B_ACC = 3 * STAGES, B_TAKEN = B_ACC + 2,
-                         B_OUT_FULL = B_TAKEN + 2, B_OUT_FREE = B_OUT_FULL + 1, B_RAW = B_OUT_FREE + 1,
-                         B_LAST = B_RAW + 1;
+                         B_RAW = B_TAKEN + 2, B_LAST = B_RAW + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * (B_LAST + 1);
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int COLS = ACCS * NX;
@@ -142,8 +140,6 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             mbar_init(&bar[C::B_ACC + i], 1);
             mbar_init(&bar[C::B_TAKEN + i], 8);
         }
-        mbar_init(&bar[C::B_OUT_FULL], 8);
-        mbar_init(&bar[C::B_OUT_FREE], 1);
         mbar_init(&bar[C::B_RAW], 1);
         mbar_init(&bar[C::B_LAST], 1);
         *sh.abort_flag = 0;
@@ -326,34 +322,25 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int quarter = warp & 3, half = (warp - 12) >> 2, r = 32 * quarter + lane;
         constexpr int CH = NX / 2;      // columns of this thread
         const uint32_t own_tm = tm + ((uint32_t)(32 * quarter) << 16) + half * CH;
-        uint8_t *out = sm + C::OFF_OUT;
-        int g = 0, stores = 0;
+        uint8_t *out = sm + C::OFF_OUT + (warp - 12) * 4096;
+        int g = 0;
         bool go = true;
-        // The staging memory is free once the store before has read it.  (Bounded waits, no block barrier: a warp that
-        // gave up would leave the others at one.)
-        const auto staging_free = [&]() {
-            if (tid == kFold) {
-                if (stores > 0) tma_store_wait();
-                mbar_arrive(&bar[C::B_OUT_FREE]);
-            }
-            return wait_inline(sh, &bar[C::B_OUT_FREE], stores & 1, kWhereSumOut);
+        // 32 values of this thread's row, at column c of the staging memory or as fp32
+        const auto stage_bf16 = [&](const float(&v)[32], int c) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(out + box_offset<2 * C::BF16_COLS>(lane, (c + i) / 8)) =
+                    make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                               pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
         };
-        // Boxes b = 0 .. n - 1 of the staging memory to columns y + step b.
-        const auto store = [&](const CUtensorMap &map, int slot, int z0, int y, int step, int n) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[C::B_OUT_FULL]);
-            if (warp == kFold / 32) {
-                if (!wait_inline(sh, &bar[C::B_OUT_FULL], stores & 1, kWhereSumOut)) return false;
-                if (lane == 0) {
-                    for (int b = 0; b < n; ++b)
-                        if (y + step * b < p.dqk) tma_store_3d(&map, out + b * 16384, y + step * b, z0, slot);
-                    tma_store_commit();
-                }
-                __syncwarp();
-            }
-            ++stores;
-            return true;
+        const auto stage_f32 = [&](const float(&v)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(out + box_offset<128>(lane, i / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        };
+        const auto store = [&](const CUtensorMap &map, const StateWalk &w, int c, int slot) {
+            const int x = w.y0 + half * CH + c, y = w.z0 + 32 * quarter;
+            staging_store(&map, out, x < p.dqk && y < p.dv, x, y, slot, lane);
         };
         for (int item = blockIdx.x; go && item < pl.items; item += gridDim.x) {
             const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
@@ -380,23 +367,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     const int n = segment_of<SEQ>(p, w, k);
                     if (k > 0 || p.init) {      // the state entering segment n
 #pragma unroll
-                        for (int round = 0; round < C::ROUNDS; ++round) {
-                            if (!(go = staging_free())) break;
+                        for (int c0 = 0; c0 < CH; c0 += C::BF16_COLS) {
+                            staging_free(lane);
 #pragma unroll
-                            for (int c0 = 0; c0 < CH / C::ROUNDS; c0 += 32) {
-                                const float(&v)[32] = x[(round * (CH / C::ROUNDS) + c0) / 32];
-#pragma unroll
-                                for (int i = 0; i < 32; i += 8) {
-                                    const int col = half * (CH / C::ROUNDS) + c0 + i;      // of this round
-                                    *reinterpret_cast<uint4 *>(out + (col / 64) * 16384 + sw128_offset(r, (col % 64) / 8)) =
-                                        make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                                                   pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
-                                }
-                            }
-                            // (two rounds: one box of each half)
-                            if (!(go = store(tmo, w.bh * p.nseg + n, w.z0, w.y0 + 64 * round, 64 * C::ROUNDS, NX / 64 / C::ROUNDS))) break;
+                            for (int c1 = 0; c1 < C::BF16_COLS; c1 += 32) stage_bf16(x[(c0 + c1) / 32], c1);
+                            store(tmo, w, c0, w.bh * p.nseg + n);
                         }
-                        if (!go) break;
                     }
                     if (k >= w.nm) break;
                     if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
@@ -425,12 +401,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (go && p.last) {
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 32) {
-                        if (!(go = staging_free())) break;
-                        const float(&v)[32] = x[c0 / 32];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(out + half * 16384 + sw128_offset(r, i / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        if (!(go = store(tml, w.bh, w.z0, w.y0 + c0, CH, 2))) break;
+                        staging_free(lane);
+                        stage_f32(x[c0 / 32]);
+                        store(tml, w, c0, w.bh);
                     }
                 }
             } else if (w.nm) {
@@ -439,25 +412,22 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if (!(go = staging_free())) break;
 #pragma unroll
                 for (int c0 = 0; c0 < CH; c0 += 32) {
                     float u[32];
                     tmem_ld32(own_tm + g % C::ACCS * NX + c0, u);
+                    staging_free(lane);
                     tmem_wait_ld();
-                    uint8_t *box = out + ((half * CH + c0) / 32) * 16384;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4 *>(box + sw128_offset(r, i / 4)) = make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                    stage_f32(u);
+                    store(tmo, w, c0, w.bh * p.nseg + w.first);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                 ++g;
-                go = store(tmo, w.bh * p.nseg + w.first, w.z0, w.y0, 32, NX / 32);
             }
         }
-        if (tid == kFold) tma_store_wait();
+        if (lane == 0) tma_store_wait();
     }
     __syncthreads();
     __syncwarp();
@@ -477,8 +447,7 @@ constexpr int kTileThreads = 640;       // TMA, two of products, one of zeros; e
 constexpr int kMaxRing = 10;
 struct TileBars {                       // indices into the barrier array; pairs are one per buffer
     static constexpr int XFULL = 0, XFREE = 2, SCORES = 4, WEIGHTS = 6, PRODUCT = 8, ENTRY = 10, SCALED = 12, DONE = 14,
-                         TAKEN = 16, TABLE = 18, OUT_FULL = 19, OUT_FREE = 20, LAST = 21, RAW = 23, ZREADY = 24 /* four */,
-                         RING = 28;
+                         TAKEN = 16, TABLE = 18, LAST = 19 /* two */, RAW = 21, ZREADY = 22 /* four */, RING = 26;
 };
 constexpr int kTileTail = 2 * kTab * 4 + (TileBars::RING + 2 * kMaxRing) * 8 + 16;
 
@@ -580,8 +549,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&bar[TileBars::TAKEN + i], kMath);
         }
         mbar_init(&bar[TileBars::TABLE], kMath);
-        mbar_init(&bar[TileBars::OUT_FULL], kMath);
-        mbar_init(&bar[TileBars::OUT_FREE], 1);
         mbar_init(&bar[TileBars::LAST], 1);
         mbar_init(&bar[TileBars::LAST + 1], 1);
         mbar_init(&bar[TileBars::RAW], 1);
@@ -904,7 +871,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // ===================== scaling of the entering state's part, read-out =====================
         const int quarter = warp & 3, half = (warp - 4 - kMath) >> 2, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const bool storer = warp == 4 + kMath;      // its first lane issues the stores
+        uint8_t *const own = out + (warp - 4 - kMath) * (64 * NZ / 2);     // 32 rows x CH columns
         constexpr int CH = NZ / 2;
         const auto run = [&]() {
             int i = 0;
@@ -934,47 +901,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (lane == 0) mbar_arrive(&bar[TileBars::SCALED + (i & 1)]);
                     if (!waitw(sh, &bar[TileBars::DONE + (i & 1)], (i >> 1) & 1, kWhereTileDone)) return;
                     tc_fence_after();
-                    // the staging memory is free once the store before has read it
-                    if (storer && lane == 0) {
-                        if (i > 0) tma_store_wait();
-                        mbar_arrive(&bar[TileBars::OUT_FREE]);
-                    }
-                    if (!waitw(sh, &bar[TileBars::OUT_FREE], i & 1, kWhereTileOut)) return;
+                    staging_free(lane);
 #pragma unroll 1
                     for (int c0 = 0; c0 < CH; c0 += 32) {
                         float x[32];
                         tmem_ld32(acc + c0, x);
                         tmem_wait_ld();
-                        const int col = half * CH + c0;
-                        uint8_t *box = out + (col / 64) * kUnit;
 #pragma unroll
                         for (int q = 0; q < 32; q += 8) {
                             uint4 v = make_uint4(pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3]),
                                                  pack_bf16x2(x[q + 4], x[q + 5]), pack_bf16x2(x[q + 6], x[q + 7]));
                             if (t >= w.len) v = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(box + sw128_offset(r, (col % 64 + q) / 8)) = v;
+                            *reinterpret_cast<uint4 *>(own + box_offset<2 * CH>(lane, (c0 + q) / 8)) = v;
                         }
                     }
                     tc_fence_before();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bar[TileBars::TAKEN + (i & 1)]);
-                        mbar_arrive(&bar[TileBars::OUT_FULL]);
-                    }
-                    if (storer) {
-                        if (!waitw(sh, &bar[TileBars::OUT_FULL], i & 1, kWhereTileOut)) return;
-                        if (lane == 0) {
-                            for (int b = 0; b < NZ / 64; ++b)
-                                if (z * NZ + 64 * b < p.dz) tma_store_3d(&tmo, out + b * kUnit, z * NZ + 64 * b, w.t0, w.bh);
-                            tma_store_commit();
-                        }
-                    }
+                    const int col = z * NZ + half * CH, row = w.t0 + 32 * quarter;
+                    staging_store(&tmo, own, col < p.dz && row < p.T, col, row, w.bh, lane);
+                    if (lane == 0) mbar_arrive(&bar[TileBars::TAKEN + (i & 1)]);
                 }
             }
         };
         run();
-        if (storer && lane == 0) tma_store_wait();
+        if (lane == 0) tma_store_wait();
     }
     __syncthreads();
     __syncwarp();
@@ -988,11 +937,10 @@ cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
     const uint64_t BH = (uint64_t)p.B * p.H;
     CUtensorMap tmz, tmy, tmo, tml;
     if (!make_tmap_3d_bf16(&tmz, p.z, p.dv, p.T, BH, 64, kStep) || !make_tmap_3d_bf16(&tmy, p.y, p.dqk, p.T, BH, 64, kStep) ||
-        !(SEQ ? make_tmap_3d_bf16(&tmo, p.states, p.dqk, p.dv, BH * p.nseg, 64, 128)
-              : make_tmap_3d_f32(&tmo, p.sums, p.dqk, p.dv, BH * p.nseg, 128)))
+        !make_tmap_store(&tmo, SEQ ? p.states : p.sums, !SEQ, p.dqk, p.dv, BH * p.nseg, SEQ ? C::BF16_COLS : 32))
         return cudaErrorInvalidValue;
     if (SEQ && p.last) {
-        if (!make_tmap_3d_f32(&tml, p.last, p.dqk, p.dv, BH, 128)) return cudaErrorInvalidValue;
+        if (!make_tmap_store(&tml, p.last, true, p.dqk, p.dv, BH, 32)) return cudaErrorInvalidValue;
     } else {
         tml = tmo;      // not used
     }
@@ -1021,7 +969,7 @@ cudaError_t tile_nz(const LinTileP &p, int32_t *status, cudaStream_t s) {
     CUtensorMap tmx, tmy, tmz, tms, tmo;
     const bool ok =
         make_tmap_3d_bf16(&tmx, p.x, p.dx, p.T, BH, 64, 128) && make_tmap_3d_bf16(&tmy, p.y, p.dx, p.T, BH, 64, 128) &&
-        make_tmap_3d_bf16(&tmz, p.z, p.dz, p.T, BH, 64, 128) && make_tmap_3d_bf16(&tmo, p.out, p.dz, p.T, BH, 64, 128) &&
+        make_tmap_3d_bf16(&tmz, p.z, p.dz, p.T, BH, 64, 128) && make_tmap_store(&tmo, p.out, false, p.dz, p.T, BH, NZ / 2) &&
         (p.state_t ? make_tmap_3d_bf16(&tms, p.states, p.dz, p.dx, BH * p.nseg, 64, 64)
                    : make_tmap_3d_bf16(&tms, p.states, p.dx, p.dz, BH * p.nseg, 64, NZ));
     if (!ok) return cudaErrorInvalidValue;

@@ -7,17 +7,25 @@
 namespace xlstm {
 namespace {
 
-// Rank-3 fp32 tensor [z][y][x], boxes of 32 x box_y x 1 with 128-byte swizzle (make_tmap_3d_bf16's counterpart).
-inline bool make_tmap_3d_f32(CUtensorMap *m, const void *base, uint64_t x, uint64_t y, uint64_t z, uint32_t box_y) {
+// Rank-3 tensor [z][y][x] for a warp's stores: boxes of 32 rows x 128 bytes (128-byte swizzle), or of 32 rows x 32 bf16
+// values (64-byte swizzle).
+inline bool make_tmap_store(CUtensorMap *m, const void *base, bool f32, uint64_t x, uint64_t y, uint64_t z, uint32_t box_x) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return false;
+    const uint64_t e = f32 ? 4 : 2;
     cuuint64_t dims[3] = {x, y, z};
-    cuuint64_t strides[2] = {x * 4, x * y * 4};
-    cuuint32_t box[3] = {32, box_y, 1};
+    cuuint64_t strides[2] = {x * e, x * y * e};
+    cuuint32_t box[3] = {box_x, 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_x * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// 16-byte chunk c of row r of such a box, rows of BYTES.
+template <int BYTES>
+__device__ __forceinline__ int box_offset(int r, int c) {
+    return BYTES == 128 ? sw128_offset(r, c) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
 // Stores a 3-D tile from 128-byte-swizzled shared memory; what lies past the tensor's extents is dropped.
@@ -58,6 +66,20 @@ __device__ __forceinline__ bool wait_inline(const Shared &sh, uint64_t *bar, uin
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until this thread's stores have read their shared memory.
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// A warp's staging memory for its stores: free once its lane 0's store before has read it; then filled by all lanes and
+// stored.  No other warp takes part.
+__device__ __forceinline__ void staging_free(int lane) {
+    if (lane == 0) tma_store_wait();
+    __syncwarp();
+}
+__device__ __forceinline__ void staging_store(const CUtensorMap *m, const void *src, bool inside, int x, int y, int z, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+        tma_store_3d(m, src, x, y, z);
+        tma_store_commit();
+    }
+}
 
 // Warp-wide: each thread reads 16 consecutive 32-bit columns of its own lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
