@@ -91,32 +91,33 @@ def tile_protocol(items, nslots: int, stages: int, nx: int, relays: int = 4) -> 
     return P
 
 
-def state_protocol(segments, stages: int, parts: int, accs: int, skip_last: bool = False) -> Protocol:
+def state_protocol(segments, stages: int, parts: int, accs: int, skip_last: bool = False, sum_stages: int = 4) -> Protocol:
     """state_tc_kernel.  segments: per tile, the stages of each of its segments in chain order; skip_last: the last
-    segment's sum is not formed.  Two groups of warps weight every other stage."""
+    segment's sum is not formed; sum_stages: stages of one sum.  Two groups of warps weight every other stage."""
     P = Protocol()
     c = g = 0
     for tile in segments:
         for si, n in enumerate(tile):
             if skip_last and si == len(tile) - 1:
                 continue
-            if g >= accs:
-                P.wait("products", f"TAKEN{g % accs}", g - accs)
-            for _ in range(n):
-                st = c % stages
-                if c >= stages:
-                    P.wait("load", f"EMPTY{st}", c - stages)
-                _copy(P, f"FULL{st}", c)
-                w = f"weights{c & 1}"
-                P.wait(w, f"FULL{st}", c)
-                if c >= parts:
-                    P.wait(w, f"EMPTY{(c - parts) % stages}", c - parts)
-                P.arrive(w, f"SCALED{st}", c)
-                P.wait("products", f"SCALED{st}", c)
-                P.arrive("products", f"EMPTY{st}", c)
-                c += 1
-            P.arrive("products", f"ACC{g % accs}", g)
-            P.wait("fold", f"ACC{g % accs}", g)
-            P.arrive("fold", f"TAKEN{g % accs}", g)
-            g += 1
+            for first in range(0, n, sum_stages):       # a sum of a few stages at a time
+                if g >= accs:
+                    P.wait("products", f"TAKEN{g % accs}", g - accs)
+                for _ in range(first, min(first + sum_stages, n)):
+                    st = c % stages
+                    if c >= stages:
+                        P.wait("load", f"EMPTY{st}", c - stages)
+                    _copy(P, f"FULL{st}", c)
+                    w = f"weights{c & 1}"
+                    P.wait(w, f"FULL{st}", c)
+                    if c >= parts:
+                        P.wait(w, f"EMPTY{(c - parts) % stages}", c - parts)
+                    P.arrive(w, f"SCALED{st}", c)
+                    P.wait("products", f"SCALED{st}", c)
+                    P.arrive("products", f"EMPTY{st}", c)
+                    c += 1
+                P.arrive("products", f"ACC{g % accs}", g)
+                P.wait("fold", f"ACC{g % accs}", g)
+                P.arrive("fold", f"TAKEN{g % accs}", g)
+                g += 1
     return P

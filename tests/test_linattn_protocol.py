@@ -35,8 +35,9 @@ def test_two_relays_are_too_few():
 @pytest.mark.parametrize("stages,parts,accs", [(4, 2, 1), (4, 2, 2), (6, 3, 2), (6, 2, 2), (8, 4, 2)])
 @pytest.mark.parametrize("segments", [[[1]], [[8, 8, 3]], [[4], [4], [1]], [[16, 16], [16, 5], [2]], [[1, 1, 1, 1]] * 3], ids=str)
 @pytest.mark.parametrize("skip_last", [False, True])
-def test_state_kernel(stages, parts, accs, segments, skip_last):
-    assert state_protocol(segments, stages, parts, accs, skip_last).check() == []
+@pytest.mark.parametrize("sum_stages", [4, 8])
+def test_state_kernel(stages, parts, accs, segments, skip_last, sum_stages):
+    assert state_protocol(segments, stages, parts, accs, skip_last, sum_stages).check() == []
 
 
 def test_planted_defects_are_caught():

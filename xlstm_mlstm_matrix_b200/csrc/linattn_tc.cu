@@ -42,9 +42,11 @@ struct RingAt {
 
 // ---- entering states -----------------------------------------------------------------------------------
 // SEQ: a block carries one 128 x NX tile of a head's state through all segments and stores it at each segment's
-// entry; the state lives in the fold warps' registers in fp32, the sum of the next segment grows in the other half of
-// tensor memory meanwhile.  Sums start from zero in every segment: the tensor core's accumulation truncates, and over a
-// whole sequence in one accumulator that would bias the state by one step of 2^-24 per 16 tokens.
+// entry; the state lives in the fold warps' registers in fp32, the next sum grows in the other half of tensor memory
+// meanwhile.  Sums start from zero every 128 tokens (256 where only entering states are formed): the tensor core's
+// accumulation truncates, which biases a sum by up to a step of 2^-24 per product added to it.  (Final states of the
+// 7B-like layer are off by 5.9e-7 of their norm, by 1.0e-6 with 256 tokens and by 8.8e-7 in plain fp32 sums; the shorter
+// sums cost 10 us of its 200.)
 // SUM (too few tiles to fill the GPU): blocks take single segments and store their sums for the chain kernel.
 constexpr int kStep = 32;                // tokens of one stage
 constexpr int kPart = 128 * kStep * 2;   // one part of the weighted rows: 8 KB
@@ -75,6 +77,9 @@ constexpr int kFold = 384;               // first thread of the fold warps
 // fold warps' (128 of them with NX = 256).
 constexpr int kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
 static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * 96, "no more than the launch brought");
+
+// Tokens of one sum.
+__device__ __forceinline__ int sum_tokens(const LinStateP &p) { return p.parts == 3 ? 128 : 256; }
 
 // One tile's walk over its segments, the same in every role.
 struct StatePlan {
@@ -209,36 +214,39 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             // The whole warp walks the work, so that descriptors stay uniform; one lane issues.
             constexpr uint32_t id_u = make_idesc(128, NX, kFmtBF16, kFmtBF16, 1, 1);
             const bool leader = elect_one();
-            const int nq = p.parts;
+            const int nq = p.parts, sum = sum_tokens(p);
             const auto run = [&]() {
                 RingAt at, part;
                 int g = 0;          // segments summed
                 for (int item = blockIdx.x; item < pl.items; item += gridDim.x) {
                     const StateWalk w = state_walk<NX, SEQ>(p, pl, item);
-                    for (int k = 0; k < w.nm; ++k, ++g) {
+                    for (int k = 0; k < w.nm; ++k) {
                         const int s0 = segment_of<SEQ>(p, w, k) * p.G, e = min(s0 + p.G, w.len);
-                        const uint32_t acc = tm + g % C::ACCS * NX;
-                        if (g >= C::ACCS && !wait_inline(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken))
-                            return;
-                        for (int t = s0; t < e; t += kStep) {
-                            if (!wait_inline(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
-                            tc_fence_after();
-                            const uint64_t z = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE), 4096, 1024);
-                            const uint64_t rest = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
-                            const uint64_t y = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE + kPart), 4096, 1024);
-                            if (leader) {
+                        for (int u0 = s0; u0 < e; u0 += sum, ++g) {
+                            const uint32_t acc = tm + g % C::ACCS * NX;
+                            if (g >= C::ACCS && !wait_inline(sh, &bar[C::B_TAKEN + g % C::ACCS], (g / C::ACCS - 1) & 1, kWhereSumTaken))
+                                return;
+                            for (int t = u0; t < min(u0 + sum, e); t += kStep) {
+                                if (!wait_inline(sh, &bar[C::B_SCALED + at.slot], at.phase, kWhereSumScaled)) return;
+                                tc_fence_after();
+                                const uint64_t z = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE), 4096, 1024);
+                                const uint64_t rest = smem_desc_sw128(smem_u32(sm + C::OFF_PARTS + part.slot * C::PARTS_BYTES), 4096, 1024);
+                                const uint64_t y = smem_desc_sw128(smem_u32(sm + at.slot * C::STAGE + kPart), 4096, 1024);
+                                if (leader) {
 #pragma unroll
-                                for (int ks = 0; ks < kStep / 16; ++ks)
+                                    for (int ks = 0; ks < kStep / 16; ++ks)
 #pragma unroll
-                                    for (int q = 0; q < 3; ++q)
-                                        if (q < nq) mma_f16_ss(acc, (q == 0 ? z : rest + (uint32_t)((q - 1) * kPart >> 4)) + (uint32_t)(ks * 2048 >> 4),
-                                                   y + (uint32_t)(ks * 2048 >> 4), id_u, t > s0 || ks > 0 || q > 0);
-                                tc_commit(&bar[C::B_EMPTY + at.slot]);
+                                        for (int q = 0; q < 3; ++q)
+                                            if (q < nq)
+                                                mma_f16_ss(acc, (q == 0 ? z : rest + (uint32_t)((q - 1) * kPart >> 4)) + (uint32_t)(ks * 2048 >> 4),
+                                                           y + (uint32_t)(ks * 2048 >> 4), id_u, t > u0 || ks > 0 || q > 0);
+                                    tc_commit(&bar[C::B_EMPTY + at.slot]);
+                                }
+                                at.next(C::STAGES);
+                                part.next(C::PARTS);
                             }
-                            at.next(C::STAGES);
-                            part.next(C::PARTS);
+                            if (leader) tc_commit(&bar[C::B_ACC + g % C::ACCS]);
                         }
-                        if (leader) tc_commit(&bar[C::B_ACC + g % C::ACCS]);
                     }
                 }
             };
@@ -321,6 +329,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         // ===================== fold =====================
         const int quarter = warp & 3, half = (warp - 12) >> 2, r = 32 * quarter + lane;
         constexpr int CH = NX / 2;      // columns of this thread
+        const int sum = sum_tokens(p);
         const uint32_t own_tm = tm + ((uint32_t)(32 * quarter) << 16) + half * CH;
         uint8_t *out = sm + C::OFF_OUT + (warp - 12) * 4096;
         int g = 0;
@@ -375,28 +384,27 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         }
                     }
                     if (k >= w.nm) break;
-                    if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
-                        go = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const float hi = n == w.nseg - 1 ? f.z : f.x, lo = n == w.nseg - 1 ? f.w : f.y;
+                    const int s0 = n * p.G, e = min(s0 + p.G, w.len);
+                    for (int u0 = s0; u0 < e; u0 += sum, ++g) {
+                        if (!(go = wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone))) break;
+                        tc_fence_after();
+                        // the segment's factor comes with its first sum
+                        const float hi = u0 > s0 ? 1.f : n == w.nseg - 1 ? f.z : f.x, lo = u0 > s0 ? 0.f : n == w.nseg - 1 ? f.w : f.y;
 #pragma unroll
-                    for (int c0 = 0; c0 < CH; c0 += 32) {
-                        float(&v)[32] = x[c0 / 32];
-#pragma unroll
-                        for (int c1 = 0; c1 < 32; c1 += 8) {
+                        for (int c0 = 0; c0 < CH; c0 += 8) {
                             float u[8];
-                            tmem_ld8(own_tm + g % C::ACCS * NX + c0 + c1, u);
+                            tmem_ld8(own_tm + g % C::ACCS * NX + c0, u);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[c1 + i] = fmaf(v[c1 + i], hi, fmaf(v[c1 + i], lo, u[i]));
+                            for (int i = 0; i < 8; ++i) {
+                                float &v = x[c0 / 32][c0 % 32 + i];
+                                v = fmaf(v, hi, fmaf(v, lo, u[i]));
+                            }
                         }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
-                    ++g;
                 }
                 if (go && p.last) {
 #pragma unroll
@@ -407,24 +415,30 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     }
                 }
             } else if (w.nm) {
-                if (!wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone)) {
-                    go = false;
-                    break;
+                const int s0 = w.first * p.G, e = min(s0 + p.G, w.len);
+                float x[CH / 32][32];
+                for (int u0 = s0; u0 < e; u0 += sum, ++g) {
+                    if (!(go = wait_inline(sh, &bar[C::B_ACC + g % C::ACCS], (g / C::ACCS) & 1, kWhereSumDone))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < CH; c0 += 8) {
+                        float u[8];
+                        tmem_ld8(own_tm + g % C::ACCS * NX + c0, u);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[c0 / 32][c0 % 32 + i] = u0 > s0 ? x[c0 / 32][c0 % 32 + i] + u[i] : u[i];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
                 }
-                tc_fence_after();
+                if (!go) break;
 #pragma unroll
                 for (int c0 = 0; c0 < CH; c0 += 32) {
-                    float u[32];
-                    tmem_ld32(own_tm + g % C::ACCS * NX + c0, u);
                     staging_free(lane);
-                    tmem_wait_ld();
-                    stage_f32(u);
+                    stage_f32(x[c0 / 32]);
                     store(tmo, w, c0, w.bh * p.nseg + w.first);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::B_TAKEN + g % C::ACCS]);
-                ++g;
             }
         }
         if (lane == 0) tma_store_wait();
