@@ -58,9 +58,15 @@ __device__ __forceinline__ void copy_rows(float *dst, const float *src, size_t p
     }
 }
 
-// acc[n][i][j] += sum_k a[M ty + i][k] b_n[4 tx + j][k]; b_n: N tiles one after another
+// Sums are held in pairs, for one instruction forms two products and their sums (the fp32 pipe takes as long for the pair as
+// for two, but half the instructions leave room for the loads: 32 heads of 2048 tokens, 128 x 128, 245 -> 216 us forward, 607 -> 528 backward).
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 lower(const float4 &v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 upper(const float4 &v) { return make_float2(v.z, v.w); }
+
+// acc[n][i][j] += sum_k a[M ty + i][k] b_n[4 tx + j][k], even k in .x and odd k in .y; b_n: N tiles one after another
 template <int M, int N>
-__device__ __forceinline__ void product_nt(float (&acc)[N][M][4], const float *a, const float *b, int ty, int tx) {
+__device__ __forceinline__ void product_nt(float2 (&acc)[N][M][4], const float *a, const float *b, int ty, int tx) {
 #pragma unroll 2
     for (int c = 0; c < kK / 4; ++c) {
         float4 av[M];
@@ -73,13 +79,40 @@ __device__ __forceinline__ void product_nt(float (&acc)[N][M][4], const float *a
                 const float4 bv = load4(b + n * kTile + at(4 * tx + j, c));
 #pragma unroll
                 for (int i = 0; i < M; ++i)
-                    acc[n][i][j] = fmaf(av[i].x, bv.x, fmaf(av[i].y, bv.y, fmaf(av[i].z, bv.z, fmaf(av[i].w, bv.w, acc[n][i][j]))));
+                    acc[n][i][j] = __ffma2_rn(lower(av[i]), lower(bv), __ffma2_rn(upper(av[i]), upper(bv), acc[n][i][j]));
             }
     }
 }
-// acc[n][i][j] += sum_k a[M ty + i][k] b[k][64 n + 4 tx + j]
+// Column j of the products above: the sum of its two sums, or half a pair.
+template <int W>
+__device__ __forceinline__ float column(const float2 (&v)[W], int j) {
+    if (W == 4) return v[W == 4 ? j : 0].x + v[W == 4 ? j : 0].y;
+    return j % 2 ? v[j / 2].y : v[j / 2].x;
+}
+// The same with one sum each, where registers do not suffice for two: acc[n][i][h] holds columns 2 h and 2 h + 1.
 template <int M, int N>
-__device__ __forceinline__ void product_nn(float (&acc)[N][M][4], const float *a, const float *b, int ty, int tx) {
+__device__ __forceinline__ void product_nt(float2 (&acc)[N][M][2], const float *a, const float *b, int ty, int tx) {
+#pragma unroll 2
+    for (int c = 0; c < kK / 4; ++c) {
+        float4 av[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) av[i] = load4(a + at(M * ty + i, c));
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 bv = load4(b + n * kTile + at(4 * tx + j, c));
+#pragma unroll
+                for (int i = 0; i < M; ++i) {
+                    float &e = j % 2 ? acc[n][i][j / 2].y : acc[n][i][j / 2].x;
+                    e = fmaf(av[i].x, bv.x, fmaf(av[i].y, bv.y, fmaf(av[i].z, bv.z, fmaf(av[i].w, bv.w, e))));
+                }
+            }
+    }
+}
+// acc[n][i][h] += sum_k a[M ty + i][k] b[k][64 n + 4 tx + 2 h .. + 1]
+template <int M, int N>
+__device__ __forceinline__ void product_nn(float2 (&acc)[N][M][2], const float *a, const float *b, int ty, int tx) {
 #pragma unroll 2
     for (int c = 0; c < kK / 4; ++c) {
         float ar[M][4];
@@ -95,10 +128,8 @@ __device__ __forceinline__ void product_nn(float (&acc)[N][M][4], const float *a
                 const float4 bv = load4(b + (4 * c + k) * 64 * N + 64 * n + 4 * tx);
 #pragma unroll
                 for (int i = 0; i < M; ++i) {
-                    acc[n][i][0] = fmaf(ar[i][k], bv.x, acc[n][i][0]);
-                    acc[n][i][1] = fmaf(ar[i][k], bv.y, acc[n][i][1]);
-                    acc[n][i][2] = fmaf(ar[i][k], bv.z, acc[n][i][2]);
-                    acc[n][i][3] = fmaf(ar[i][k], bv.w, acc[n][i][3]);
+                    acc[n][i][0] = __ffma2_rn(both(ar[i][k]), lower(bv), acc[n][i][0]);
+                    acc[n][i][1] = __ffma2_rn(both(ar[i][k]), upper(bv), acc[n][i][1]);
                 }
             }
     }
@@ -133,21 +164,19 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
     }
     copies_wait<0>();
     __syncthreads();
-    float acc[N][M][4] = {};
+    float2 acc[N][M][2] = {};
 #pragma unroll 4
     for (int s = 0; s < kSeg; ++s) {
-        float a[M];
+        float2 a[M];
 #pragma unroll
-        for (int i = 0; i < M; ++i) a[i] = ws[s] * Zs[s * R + M * ty + i];
+        for (int i = 0; i < M; ++i) a[i] = both(ws[s] * Zs[s * R + M * ty + i]);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
             const float4 b = load4(Ys + s * 64 * N + 64 * c + 4 * tx);
 #pragma unroll
             for (int i = 0; i < M; ++i) {
-                acc[c][i][0] = fmaf(a[i], b.x, acc[c][i][0]);
-                acc[c][i][1] = fmaf(a[i], b.y, acc[c][i][1]);
-                acc[c][i][2] = fmaf(a[i], b.z, acc[c][i][2]);
-                acc[c][i][3] = fmaf(a[i], b.w, acc[c][i][3]);
+                acc[c][i][0] = __ffma2_rn(a[i], lower(b), acc[c][i][0]);
+                acc[c][i][1] = __ffma2_rn(a[i], upper(b), acc[c][i][1]);
             }
         }
     }
@@ -159,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
             const int r = z0 + M * ty + i, col = y0 + 64 * c + 4 * tx;
             if (r < p.dv && col < p.dqk)
                 store4(U + (size_t)r * p.dqk + col,
-                       make_float4(acc[c][i][0], acc[c][i][1], acc[c][i][2], acc[c][i][3]));
+                       make_float4(acc[c][i][0].x, acc[c][i][0].y, acc[c][i][1].x, acc[c][i][1].y));
         }
 }
 
@@ -245,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
     // the call's last kernel: no wait of this path can fail
     if (blockIdx.x == 0 && tid < 4) status[tid] = 0;
     float *out = static_cast<float *>(p.out) + (size_t)bh * p.T * p.dz;
-    float acc[N][M][4] = {};
+    float2 acc[N][M][2] = {};
     if (t0 + r0 < len) {
         const float ld = head_log_decay(p.log_decay, bh % p.H);
         const int e = min(t0 + kSeg, len), rows = e - t0;
@@ -280,7 +309,11 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
 #pragma unroll
         for (int st = 0; st < S::STEPS - 1; ++st) fetch(st);
         for (int i = tid; i <= kSeg; i += kThreads) pw[i] = decay_pow(ld, i);
-        float sc[1][M][4] = {};
+        // Scores, and the entering state's part: two sums each at N = 1; at N = 4 the part goes into acc itself, for the
+        // registers (two sums there: 882 us for 64 heads of 1024 tokens, 256 x 256, not 691).
+        constexpr int W = N == 1 ? 4 : 2;
+        constexpr bool APART = N < 4;
+        float2 sc[1][M][W] = {}, part[N][M][W] = {};
         for (int st = 0; st < total; ++st) {
             copies_wait<S::STEPS - 2>();
             __syncthreads();
@@ -290,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
                 product_nt<M, 1>(sc, A, Yt, ty, tx);
                 if (entry) {
                     if (p.state_t) product_nn<M, N>(acc, A, Bt, ty, tx);
+                    else if constexpr (APART) product_nt<M, N>(part, A, Bt, ty, tx);
                     else product_nt<M, N>(acc, A, Bt, ty, tx);
                 }
                 if (st == nk - 1) {
@@ -300,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int t = r0 + M * ty + i, s = 4 * tx + j, far = p.rev ? s - t : t - s;
-                            w[j] = far >= 0 && s < rows ? p.scale * pw[far] * sc[0][i][j] : 0.f;
+                            w[j] = far >= 0 && s < rows ? p.scale * pw[far] * column<W>(sc[0][i], j) : 0.f;
                         }
                         store4(Ps + (tx >> 3) * kTile + at(M * ty + i, tx & 7), make_float4(w[0], w[1], w[2], w[3]));
                         const int r = r0 + M * ty + i;
@@ -308,7 +342,13 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
 #pragma unroll
                         for (int c = 0; c < N; ++c)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[c][i][j] *= rho;
+                            for (int h = 0; h < 2; ++h)
+                                {
+                                if (APART)
+                                    acc[c][i][h] = __fadd2_rn(acc[c][i][h], make_float2(column<W>(part[c][i], 2 * h),
+                                                                                        column<W>(part[c][i], 2 * h + 1)));
+                                acc[c][i][h] = __fmul2_rn(acc[c][i][h], both(rho));
+                            }
                     }
                 }
             } else {
@@ -327,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) tile_kernel(const __
             const int col = z0 + 64 * c + 4 * tx;
             if (col < p.dz)
                 store4(out + (size_t)t * p.dz + col,
-                       t < len ? make_float4(acc[c][i][0], acc[c][i][1], acc[c][i][2], acc[c][i][3])
+                       t < len ? make_float4(acc[c][i][0].x, acc[c][i][0].y, acc[c][i][1].x, acc[c][i][1].y)
                                : make_float4(0.f, 0.f, 0.f, 0.f));
         }
     }
