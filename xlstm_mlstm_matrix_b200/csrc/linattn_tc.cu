@@ -55,7 +55,8 @@ template <int NX, bool SEQ>
 struct StateCfg {
     static constexpr int ACCS = 2;      // two sums take turns in tensor memory
     // A place holds a stage from the start of its loads (some 2000 cycles) through its weighting (as long) to the end of
-    // its products (400 to 800).  The first part takes the place of z; the others have PARTS places of their own.
+    // its products (400 to 800).  The first part takes the place of z; the others have PARTS places of their own.  (Four
+    // places and two for all three parts, NX = 256: 211 us, so 200.)
     static constexpr int STAGES = NX == 256 ? 6 : 8, PARTS = STAGES / 2;
     static constexpr int Y_BYTES = NX * kStep * 2;
     static constexpr int STAGE = kPart + Y_BYTES;               // z and y as they come
@@ -74,7 +75,8 @@ struct StateCfg {
 constexpr int kStateThreads = 640;       // TMA, MMA, two idle warps; two groups of four warps of weights; eight fold warps
 constexpr int kFold = 384;               // first thread of the fold warps
 // Registers per thread of the three kinds, out of the 96 each that 640 threads are launched with: the state lives in the
-// fold warps' (128 of them with NX = 256).
+// fold warps' (128 of them with NX = 256).  With the state in tensor memory instead there is room for one sum only, and the
+// products waited while it was folded in (7B-like layer's states 232 us, so 211).
 constexpr int kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
 static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * 96, "no more than the launch brought");
 
