@@ -149,6 +149,20 @@ def test_no_sequence_has_a_token(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_views(dtype):
+    """Decays and lengths at any 4-byte address, the other tensors at any 16-byte address."""
+    x = make(3, 2, 200, 64, 64, dtype, seed=62, lens=[200, 7, 130])
+    want = check_fwd(x)
+    off = lambda t, n: torch.cat([t.new_zeros(n), t.flatten()])[n:].view(t.shape)  # noqa: E731
+    n = 16 // x["q"].element_size()
+    y = {m: off(x[m], n) for m in ("q", "k", "v")}
+    o, C = capi.linattn_fwd(**y, log_decay=off(x["log_decay"], 1), state=off(x["state"], 4), lens=off(x["lens"], 3))
+    assert torch.equal(o, want[0]) and torch.equal(C, want[1])
+    with pytest.raises(capi.XlstmError):
+        capi.linattn_fwd(off(x["q"], 1), x["k"], x["v"], x["log_decay"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_many_sequences(dtype):
     """More heads than a grid's second axis holds."""
     x = make(70001, 1, 3, 16, 16, dtype, seed=61)

@@ -1,6 +1,7 @@
 // One token of the linear attention with a decay per head: C' = l C + v k^T, o = scale C' q.
 //
-// Bound by the state's bytes: d_v x d_qk fp32 per head are read and written once.  A block owns a range
+// Bound by the state's bytes: d_v x d_qk fp32 per head are read and written once (128 x 8 heads of 256 x 512: 172 to 184 us,
+// 5.9 to 6.3 TB/s).  A block owns a range
 // of rows of one head; the lanes of a warp cover whole rows with 16-byte accesses, all loads of a lane's
 // rows issued before any is used.
 #include "linattn.cuh"
@@ -96,7 +97,7 @@ cudaError_t launch_linattn_step(const LinAttnArgs &a, cudaStream_t s) {
     p.H = a.H; p.dqk = a.dqk; p.dv = a.dv; p.scale = a.scale;
     p.q = a.q; p.k = a.k; p.v = a.v; p.log_decay = a.log_decay; p.C = a.C0; p.o = a.o; p.C1 = a.C1;
     // rows are independent, so a head splits over blocks, in place too: eight blocks per SM while a block
-    // keeps 16 rows
+    // keeps 16 rows (64 x 8 heads of 128 x 128: 19.5 us; with two per SM 21.1, with 32 20.5)
     const long long BH = (long long)a.B * a.H, target = 8LL * sm_count();
     int split = 1;
     while (BH * split < target && a.dv / (split * 2) >= 16) split *= 2;

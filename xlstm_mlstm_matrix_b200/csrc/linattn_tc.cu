@@ -480,7 +480,7 @@ struct TilePlan {
 // The items of a block, the same in every role: rounds over the grid, turned by 37 blocks each so that a block meets every
 // place within the segments (whose tiles have between one and G / 128 units).  A warp looks 32 rounds up at a time, a round
 // per lane, and hands the lanes' items out: looked up one by one, the lengths' and decays' latency was most of the time of
-// short items (4096 items without a live token: 49 us, now 13).
+// short items (4096 items without a live token: 49 us, so 13).
 struct TileWalk {
     int next;                          // round of the next look-up
     unsigned mask;                     // lanes whose item is still to come
