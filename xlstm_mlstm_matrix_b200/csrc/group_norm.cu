@@ -411,15 +411,20 @@ __global__ void __launch_bounds__(kThreads) group_norm_sums_kernel(const float *
     }
 }
 
-int lanes_per_row(int D) {
+// Accesses of eight channels per lane.  bf16: two, for a row's sums over its lanes cost about as much as eight channels do
+// (16 x 8 x 4096 groups of 256: 139 us forward and 249 backward, 164 and 315 with one).  With fp32 tensors the bytes weigh
+// more and shared memory holds fewer rows: one, up to 256 channels (8 x 8 x 2048 groups of 256, backward: 179 us, 185 with two).
+constexpr int accesses(int D, bool bf16) { return D > 256 || (bf16 && D > 16) ? 2 : 1; }
+int lanes_per_row(int D, bool bf16) {
     int l = 2;
-    while (l < 32 && l * kV < D) l *= 2;
+    while (l < 32 && accesses(D, bf16) * l * kV < D) l *= 2;
     return l;
 }
+bool all_bf16(const xlstm_group_norm_desc_t *d) { return d->x_dtype == XLSTM_BF16 && d->y_dtype == XLSTM_BF16; }
 // Tokens of one block: at least one pass of its warps, and about `target` blocks in all.
-int tokens_per_block(int tokens, int G, int D, long long target) {
-    const int pass = kWarps * (32 / lanes_per_row(D));
-    const long long per = ((long long)tokens * G + target - 1) / target;
+int tokens_per_block(const xlstm_group_norm_desc_t *d, long long target) {
+    const int pass = kWarps * (32 / lanes_per_row(d->D, all_bf16(d)));
+    const long long per = ((long long)d->B * d->T * d->G + target - 1) / target;
     return (int)((per + pass - 1) / pass * pass);
 }
 // Forward: some blocks per SM more than the three that run at a time even out their ends (7B-like layer 139 us with 3 to
@@ -430,7 +435,7 @@ constexpr long long kFwdBlocks = 148 * 8;
 constexpr long long kBwdBlocks = 148 * 2;   // also bounds the partial sums
 
 int bwd_chunks(const xlstm_group_norm_desc_t *d) {
-    const int tokens = d->B * d->T, tpb = tokens_per_block(tokens, d->G, d->D, kBwdBlocks);
+    const int tokens = d->B * d->T, tpb = tokens_per_block(d, kBwdBlocks);
     return (tokens + tpb - 1) / tpb;
 }
 
@@ -444,13 +449,16 @@ cudaError_t launch(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
 }
 template <typename Tx, typename Ty, bool kBwd>
 cudaError_t launch_types(const GroupNormP &p, unsigned blocks, cudaStream_t s) {
+    constexpr bool bf16 = sizeof(Tx) + sizeof(Ty) == 4;
+    constexpr int NV = accesses(256, bf16);       // of most widths
+    if (p.D == 16) return launch<Tx, Ty, 2, 1, kBwd>(p, blocks, s);
     if (p.D > 256) return launch<Tx, Ty, 32, 2, kBwd>(p, blocks, s);
-    switch (lanes_per_row(p.D)) {
-        case 2: return launch<Tx, Ty, 2, 1, kBwd>(p, blocks, s);
-        case 4: return launch<Tx, Ty, 4, 1, kBwd>(p, blocks, s);
-        case 8: return launch<Tx, Ty, 8, 1, kBwd>(p, blocks, s);
-        case 16: return launch<Tx, Ty, 16, 1, kBwd>(p, blocks, s);
-        default: return launch<Tx, Ty, 32, 1, kBwd>(p, blocks, s);
+    switch (lanes_per_row(p.D, bf16)) {
+        case 2: return launch<Tx, Ty, 2, NV, kBwd>(p, blocks, s);
+        case 4: return launch<Tx, Ty, 4, NV, kBwd>(p, blocks, s);
+        case 8: return launch<Tx, Ty, 8, NV, kBwd>(p, blocks, s);
+        case 16: return launch<Tx, Ty, 16, NV, kBwd>(p, blocks, s);
+        default: return launch<Tx, Ty, 32, NV, kBwd>(p, blocks, s);
     }
 }
 template <bool kBwd>
@@ -479,7 +487,7 @@ GroupNormP pack(const xlstm_group_norm_desc_t *d, long long blocks) {
     GroupNormP p{};
     p.B = d->B; p.T = d->T; p.G = d->G; p.D = d->D; p.heads_major = d->x_layout == XLSTM_HEADS_MAJOR;
     p.act = d->act; p.eps = d->eps; p.tokens = d->B * d->T;
-    p.tokens_per_block = tokens_per_block(p.tokens, d->G, d->D, blocks);
+    p.tokens_per_block = tokens_per_block(d, blocks);
     p.inv_D = 1.f / (float)d->D;
     p.by_T = fast_div((uint32_t)d->T);
     return p;
