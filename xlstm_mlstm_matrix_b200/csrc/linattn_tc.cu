@@ -77,8 +77,8 @@ constexpr int kFold = 384;               // first thread of the fold warps
 // Registers per thread of the three kinds, out of the 96 each that 640 threads are launched with: the state lives in the
 // fold warps' (128 of them with NX = 256).  With the state in tensor memory instead there is room for one sum only, and the
 // products waited while it was folded in (7B-like layer's states 232 us, so 211).
-constexpr int kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
-static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * 96, "no more than the launch brought");
+constexpr int kLaunchRegs = 96, kIoRegs = 40, kWeightRegs = 48, kFoldRegs = 168;
+static_assert(kIoRegs + 2 * kWeightRegs + 2 * kFoldRegs <= 5 * kLaunchRegs, "no more than the launch brought");
 
 // Tokens of one sum.
 __device__ __forceinline__ int sum_tokens(const LinStateP &p) { return p.parts == 3 ? 128 : 256; }
@@ -961,6 +961,12 @@ cudaError_t state_nx(const LinStateP &p, int32_t *status, cudaStream_t s) {
         tml = tmo;      // not used
     }
     auto *const kernel = state_tc_kernel<NX, SEQ>;
+    // launched with fewer registers the fold warps would wait for theirs for good
+    static const bool enough = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, state_tc_kernel<NX, SEQ>) == cudaSuccess && at.numRegs >= kLaunchRegs;
+    }();
+    if (!enough) return cudaErrorInvalidKernelImage;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
     if (e != cudaSuccess) return e;
     const int zt = (p.dv + 127) / 128, yt = (p.dqk + NX - 1) / NX;
