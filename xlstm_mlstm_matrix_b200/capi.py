@@ -463,14 +463,16 @@ def bwd(q, k, v, i_pre, f_pre, dh, state=None, dstate=None, qk_scale=None, strea
 # are, addresses go to ctypes as plain integers, and a shape's descriptor and workspace size are formed once.
 _torch = None          # the torch module, once a helper has been called (importing this module loads nothing)
 _current_stream = None     # CUDA device index -> its current stream's handle
+_current_device = None     # -> the current CUDA device's index
 
 
 def _load_torch():
-    global _torch, _current_stream
+    global _torch, _current_stream, _current_device
     import torch
-    # the handle without a stream object around it, where this torch offers it
+    # the handle without a stream object around it, the index without a check, where this torch offers them
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _current_stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return torch
 
@@ -497,7 +499,7 @@ def _run(fn, index, stream, *args):
     if index < 0:
         raise ValueError("CUDA tensors expected")
     stream = _current_stream(index) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-    if _torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, stream)
     else:
         with _torch.cuda.device(index):
@@ -542,9 +544,12 @@ def _linattn_inputs(q, k, v, log_decay, state, lens, scale, axes):
         _want(k, "k", shape, dt, index)
     if v.dtype != dt or v.shape != plan[3] or v.get_device() != index or not v.is_contiguous():
         _want(v, "v", plan[3], dt, index)
-    _want(log_decay, "log_decay", plan[6], torch.float32, index)
-    if state is not None:
-        _want(state, "state", plan[4], torch.float32, index)
+    f32, l = torch.float32, log_decay
+    if l.dtype != f32 or l.shape != plan[6] or l.get_device() != index or not l.is_contiguous():
+        _want(l, "log_decay", plan[6], f32, index)
+    if state is not None and (state.dtype != f32 or state.shape != plan[4] or state.get_device() != index
+                              or not state.is_contiguous()):
+        _want(state, "state", plan[4], f32, index)
     if lens is not None:
         _want(lens, "lens", plan[5], torch.int32, index)
     return torch, index, plan
